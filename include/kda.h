@@ -339,6 +339,174 @@ kda_status_t kda_recurrent_fwd(const kda_shape_t* shape, const void* q, const vo
 kda_status_t kda_selftest_bounded_wait(int32_t* dev_status, uint32_t budget_us, int32_t complete,
                                        void* stream);
 
+/* ===================================================================================
+ * The recurrent block's other operators: the short causal convolution in front of a
+ * recurrence, the selective state space scan (the diagonal linear recurrence beside
+ * KDA's delta rule), and layer norm.  The conventions of the top of this file hold,
+ * with these additions:
+ *   - "Rows" are the B*T token rows of a dense batch, or the T packed rows of a varlen
+ *     batch (cu_seqlens as in kda_chunk_fwd: device int32 [num_seqs + 1], B == 1).
+ *     Sequence n starts from its own state and never sees another sequence's rows.
+ *     Rows that no sequence covers are left untouched.  An inconsistent cu_seqlens sets
+ *     KDA_DEV_BAD_SEQLENS; the sequences it affects are skipped.
+ *   - The inputs named with a stride may be columns of a wider row-major matrix: the
+ *     stride is the distance of consecutive rows in elements (0: rows are contiguous).
+ *     Everything else is contiguous.
+ *   - Every pointer needs its element's alignment.  Where the pointers, strides and
+ *     row lengths are multiples of 16 bytes, 16-byte accesses are used.
+ *   - Activations and their gradients have the element type `dtype` (fp32 or bf16);
+ *     parameters, their gradients and recurrent states are fp32.  All arithmetic is fp32,
+ *     rounded once where a bf16 output is stored.  No sum uses atomics: results do not
+ *     vary from run to run.
+ *   - workspace: as kda_chunk_fwd (256-byte aligned, or NULL: taken from the
+ *     stream-ordered pool and returned on `stream`).
+ * =================================================================================== */
+
+/*
+ * Short causal depthwise convolution of W = width taps, optionally followed by SiLU:
+ *     pre[t, d] = bias[d] + sum_{j=0}^{W-1} weight[d, j] * x[t - (W-1) + j, d]
+ *     out[t, d] = pre / (1 + e^{-pre})   (activation 1)   or   pre   (activation 0)
+ * Inputs before a sequence's first row come from its state, the W - 1 inputs that
+ * preceded it (oldest first), or are zero.
+ */
+typedef struct {
+    int32_t B;           /* sequences (dense); 1 for varlen; step: sequences */
+    int32_t T;           /* rows per sequence (dense) or in total (varlen); step: 1 */
+    int32_t D;           /* channels */
+    int32_t num_seqs;    /* B for dense, len(cu_seqlens) - 1 for varlen */
+    int32_t width;       /* W, 2 to 8 */
+    int32_t dtype;       /* kda_dtype_t of x, out, the states and dx */
+    int32_t grad_dtype;  /* kda_dtype_t of d_out (bwd): `dtype`, or KDA_F32 */
+    int32_t activation;  /* 0: none, 1: SiLU */
+    int64_t x_stride;    /* elements between rows of x (0: D) */
+    int32_t* dev_status; /* optional device int32, see KDA_DEV_* */
+} kda_conv_shape_t;
+
+/*
+ * kda_conv_fwd -- x [rows, D], weight [D, W] fp32, bias [D] fp32 or NULL,
+ * state0 [num_seqs, W-1, D] or NULL (zero) -> out [rows, D],
+ * stateT [num_seqs, W-1, D] or NULL: the last W - 1 inputs of every sequence (of
+ * state0 followed by its rows), copied bit for bit.
+ */
+kda_status_t kda_conv_fwd(const kda_conv_shape_t* shape, const void* x, const float* weight,
+                          const float* bias, const void* state0, const int32_t* cu_seqlens,
+                          void* out, void* stateT, void* stream);
+
+/* kda_conv_step -- one row for each of B sequences (T == 1): x, out [B, D];
+ * state [B, W-1, D] is read, shifted by the new input and written in place. */
+kda_status_t kda_conv_step(const kda_conv_shape_t* shape, const void* x, const float* weight,
+                           const float* bias, void* state, void* out, void* stream);
+
+/*
+ * kda_conv_bwd -- gradients of kda_conv_fwd for sum(out * d_out) + sum(stateT * d_stateT).
+ * d_out [rows, D] of grad_dtype; d_stateT [num_seqs, W-1, D] of dtype or NULL (zero).
+ * Writes dx [rows, D] (dtype), dweight [D, W] (fp32), dbias [D] (fp32, or NULL),
+ * dstate0 [num_seqs, W-1, D] (dtype, or NULL).  Nothing but the inputs is needed: the
+ * pre-activation is computed again.
+ */
+kda_status_t kda_conv_bwd(const kda_conv_shape_t* shape, const void* x, const float* weight,
+                          const float* bias, const void* state0, const int32_t* cu_seqlens,
+                          const void* d_out, const void* d_stateT, void* dx, float* dweight,
+                          float* dbias, void* dstate0, void* workspace, size_t workspace_bytes,
+                          void* stream);
+size_t kda_conv_bwd_workspace_size(const kda_conv_shape_t* shape);
+
+/*
+ * Selective state space scan.  Per channel d with N states:
+ *     dt[t, d]   = softplus(delta[t, d] + delta_bias[d])     (softplus 1; else without it)
+ *     h[t, d, n] = exp(dt[t, d] A[d, n]) h[t-1, d, n] + dt[t, d] x[t, d] Bm[t, g, n]
+ *     y[t, d]    = sum_n h[t, d, n] Cm[t, g, n] + Dskip[d] x[t, d]
+ *     out[t, d]  = y z / (1 + e^{-z})                        (z given; else y)
+ * The D channels form G groups; channel d reads row g = d / (D / G) of Bm and Cm.
+ */
+typedef struct {
+    int32_t B;           /* sequences (dense); 1 for varlen; step: sequences */
+    int32_t T;           /* rows per sequence (dense) or in total (varlen); step: 1 */
+    int32_t D;           /* channels */
+    int32_t N;           /* states per channel, 1 to 128 */
+    int32_t G;           /* groups, dividing D */
+    int32_t num_seqs;    /* B for dense, len(cu_seqlens) - 1 for varlen */
+    int32_t dtype;       /* kda_dtype_t of x, delta, z, Bm, Cm, out and their gradients */
+    int32_t softplus;    /* 1: dt = softplus(delta + bias), 0: dt = delta + bias */
+    int64_t x_stride;    /* elements between rows (0: D) */
+    int64_t delta_stride;
+    int64_t z_stride;
+    int64_t b_stride;    /* elements between rows of Bm (0: G*N) */
+    int64_t c_stride;
+    int32_t* dev_status; /* optional device int32, see KDA_DEV_* */
+} kda_ssm_shape_t;
+
+/*
+ * kda_ssm_fwd -- x, delta [rows, D]; A [D, N] fp32; Bm, Cm [rows, G, N]; Dskip [D] fp32
+ * or NULL; z [rows, D] or NULL; delta_bias [D] fp32 or NULL; h0 [num_seqs, D, N] fp32 or
+ * NULL (zero) -> out [rows, D], hT [num_seqs, D, N] fp32 or NULL (not wanted).
+ * With too few sequences and channels to fill the GPU the rows are cut into segments:
+ * one pass gives every segment's own state, a short one joins them, and the last pass
+ * runs each segment from its incoming state (workspace: those states).
+ */
+kda_status_t kda_ssm_fwd(const kda_ssm_shape_t* shape, const void* x, const void* delta,
+                         const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                         const void* z, const float* delta_bias, const float* h0,
+                         const int32_t* cu_seqlens, void* out, float* hT, void* workspace,
+                         size_t workspace_bytes, void* stream);
+/* Bytes of workspace (0: none needed); varlen != 0 when a cu_seqlens will be passed. */
+size_t kda_ssm_fwd_workspace_size(const kda_ssm_shape_t* shape, int varlen);
+
+/* kda_ssm_step -- one row for each of B sequences (T == 1): x, delta, z, out [B, D],
+ * Bm, Cm [B, G, N]; h [B, D, N] fp32 is read and overwritten with the new state. */
+kda_status_t kda_ssm_step(const kda_ssm_shape_t* shape, const void* x, const void* delta,
+                          const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                          const void* z, const float* delta_bias, float* h, void* out,
+                          void* stream);
+
+/*
+ * kda_ssm_bwd -- gradients of kda_ssm_fwd for sum(out * d_out) + sum(hT * d_hT).
+ * d_out [rows, D] (dtype); d_hT [num_seqs, D, N] fp32 or NULL (zero).  Writes dx, ddelta
+ * [rows, D], dB, dC [rows, G, N], dz [rows, D] (with z; else NULL) of dtype, and fp32 dA
+ * [D, N], dDskip [D] (with Dskip; else NULL), ddelta_bias [D] (with delta_bias; else
+ * NULL), dh0 [num_seqs, D, N] or NULL (not wanted).  The states are computed again from
+ * the inputs; nothing is kept from the forward call.
+ */
+kda_status_t kda_ssm_bwd(const kda_ssm_shape_t* shape, const void* x, const void* delta,
+                         const float* A, const void* Bm, const void* Cm, const float* Dskip,
+                         const void* z, const float* delta_bias, const float* h0,
+                         const int32_t* cu_seqlens, const void* d_out, const float* d_hT,
+                         void* dx, void* ddelta, float* dA, void* dB, void* dC, float* dDskip,
+                         void* dz, float* ddelta_bias, float* dh0, void* workspace,
+                         size_t workspace_bytes, void* stream);
+size_t kda_ssm_bwd_workspace_size(const kda_ssm_shape_t* shape, int varlen);
+
+/*
+ * Layer norm over the last axis of x [rows, groups, D]:
+ *     mean = sum_d x / D,  rstd = (sum_d (x - mean)^2 / D + eps)^{-1/2}
+ *     out[r, g, d] = (x - mean) rstd weight[g, d] + bias[g, d]
+ * groups = 1 is the norm of a token's row; groups = H, D = d_v the norm of every head of
+ * a recurrence's output, with weights per head.
+ */
+typedef struct {
+    int64_t rows;
+    int32_t groups;
+    int32_t D;           /* 1 to 32768 */
+    int32_t dtype;       /* kda_dtype_t of x, out, d_out and dx */
+    float eps;           /* >= 0 (fwd) */
+    int64_t x_stride;    /* elements between rows of x (0: groups*D); groups are contiguous */
+} kda_norm_shape_t;
+
+/* kda_layer_norm_fwd -- weight, bias [groups, D] fp32, each or NULL (ones, zeros);
+ * mean, rstd [rows, groups] fp32, both or neither NULL (not wanted). */
+kda_status_t kda_layer_norm_fwd(const kda_norm_shape_t* shape, const void* x, const float* weight,
+                                const float* bias, void* out, float* mean, float* rstd,
+                                void* stream);
+
+/* kda_layer_norm_bwd -- gradients of kda_layer_norm_fwd for sum(out * d_out), from the
+ * mean and rstd that it returned: dx [rows, groups, D] (dtype, contiguous); dweight,
+ * dbias [groups, D] fp32, each or NULL (not wanted). */
+kda_status_t kda_layer_norm_bwd(const kda_norm_shape_t* shape, const void* d_out, const void* x,
+                                const float* weight, const float* mean, const float* rstd,
+                                void* dx, float* dweight, float* dbias, void* workspace,
+                                size_t workspace_bytes, void* stream);
+size_t kda_layer_norm_bwd_workspace_size(const kda_norm_shape_t* shape);
+
 /* Human-readable text for a status code (static storage). */
 const char* kda_status_str(kda_status_t status);
 

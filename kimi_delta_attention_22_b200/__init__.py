@@ -83,6 +83,7 @@ def load_library(path: str | None = None):
     lib.kda_version.restype = ctypes.c_char_p
     lib.kda_selftest_bounded_wait.argtypes = [P, ctypes.c_uint32, ctypes.c_int32, P]
     lib.kda_selftest_bounded_wait.restype = ctypes.c_int
+    block_ops.declare(lib)
     if path is None:
         _lib = lib
     return lib
@@ -373,3 +374,9 @@ def kda_selftest_bounded_wait(dev_status: torch.Tensor, budget_us: int, complete
                                        _stream_handle(dev_status.device))
     if st != 0:
         raise KDAError(st, "kda_selftest_bounded_wait")
+
+
+from . import block_ops  # noqa: E402  (takes the names above)
+from .block_ops import *  # noqa: E402,F401,F403
+
+__all__ += block_ops.__all__

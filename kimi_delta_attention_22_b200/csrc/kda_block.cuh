@@ -1,0 +1,241 @@
+// kda_block.cuh -- launch interfaces and device helpers of the recurrent block's
+// operators (short causal convolution, selective state space scan, layer norm).
+#pragma once
+
+#include "kda_internal.cuh"
+
+namespace kda {
+
+constexpr int kSMs = 148;   // B200
+
+struct ConvArgs {
+    const void* x;
+    const float* w;
+    const float* bias;
+    const void* state0;
+    const int32_t* cu;
+    void* out;
+    void* stateT;
+    // backward
+    const void* d_out;
+    const void* d_stateT;
+    void* dx;
+    float* dw;
+    float* db;
+    void* dstate0;
+    float* part;
+    int32_t* dev_status;
+    long long M, T;      // rows in all, rows per sequence (dense)
+    long long xs;        // row stride of x
+    int D, W, num_seqs;
+};
+
+cudaError_t launch_conv_fwd(const ConvArgs& a, bool bf16, bool silu, cudaStream_t s);
+cudaError_t launch_conv_step(const ConvArgs& a, bool bf16, bool silu, cudaStream_t s);
+cudaError_t launch_conv_bwd(const ConvArgs& a, bool bf16, bool grad_bf16, bool silu, cudaStream_t s);
+size_t conv_bwd_workspace_bytes(long long M, int D, int W);
+
+struct SsmArgs {
+    const void* x;
+    const void* delta;
+    const float* A;
+    const void* Bm;
+    const void* Cm;
+    const float* Dskip;
+    const void* z;
+    const float* delta_bias;
+    const float* h0;
+    const int32_t* cu;
+    void* out;
+    float* hT;
+    // backward
+    const void* d_out;
+    const float* d_hT;
+    void* dx;
+    void* ddelta;
+    float* dA;
+    void* dB;
+    void* dC;
+    float* dDskip;
+    void* dz;
+    float* ddelta_bias;
+    float* dh0;
+    uint8_t* ws;
+    int32_t* dev_status;
+    long long M, T;      // rows in all, rows per sequence (dense)
+    long long xs, ds, zs, bs, cs;   // row strides
+    int D, N, G, num_seqs, softplus;
+};
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, bool bf16, cudaStream_t s);
+size_t ssm_fwd_workspace_bytes(long long B, long long T, int D, int N, int G, bool varlen);
+cudaError_t launch_ssm_step(const SsmArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_ssm_bwd(const SsmArgs& a, bool bf16, cudaStream_t s);
+size_t ssm_bwd_workspace_bytes(long long B, long long T, int D, int N, int G);
+
+struct NormArgs {
+    const void* x;
+    const float* w;
+    const float* b;
+    void* out;
+    float* mean;
+    float* rstd;
+    const void* d_out;
+    void* dx;
+    float* dw;
+    float* db;
+    float* part;
+    long long rows, xs;
+    int G, D;
+    float eps;
+};
+
+cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
+cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t s);
+size_t norm_bwd_workspace_bytes(long long rows, int G, int D);
+
+// out_i[c] = sum_k part[k][off_i + c], k in order within each of eight interleaved
+// partial sums: the second stage of a parameter gradient's reduction over the rows.
+cudaError_t launch_colsum(const float* part, int K, long long n0, float* out0, long long n1, float* out1,
+                          long long n2, float* out2, cudaStream_t s);
+
+// ------------------------------------------------------------------ device helpers
+
+struct SeqRange {
+    long long b, e;   // rows [b, e)
+    int q;            // sequence
+    bool ok;          // row t lies in a sequence whose bounds are consistent
+};
+
+// The sequence of row t (0 <= t < M).  Dense: t / T.  Packed: the last n with
+// cu[n] <= t, which skips empty sequences; bounds that break the rules give ok = false,
+// so that no address is ever formed from them.
+__device__ __forceinline__ SeqRange find_seq(const int32_t* cu, int n, long long M, long long T, long long t) {
+    SeqRange r;
+    if (cu == nullptr) {
+        r.q = (int)(t / T);
+        r.b = (long long)r.q * T;
+        r.e = r.b + T;
+        r.ok = true;
+        return r;
+    }
+    int lo = 0, hi = n;   // the last i in [0, n) with cu[i] <= t, or 0
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
+    }
+    r.q = lo;
+    r.b = __ldg(cu + lo);
+    r.e = __ldg(cu + lo + 1);
+    r.ok = r.b >= 0 && r.b <= t && t < r.e && r.e <= M && !(lo == 0 && r.b != 0);
+    return r;
+}
+
+// Bounds of sequence q with the same rules as find_seq; flags a broken one.
+__device__ __forceinline__ bool check_seq(const int32_t* cu, int q, long long M, long long T, int32_t* dev_status,
+                                          long long& b, long long& e) {
+    if (cu == nullptr) {
+        b = (long long)q * T;
+        e = b + T;
+        return true;
+    }
+    b = __ldg(cu + q);
+    e = __ldg(cu + q + 1);
+    if (b < 0 || e < b || e > M || (q == 0 && b != 0)) {
+        if (dev_status) atomicOr(dev_status, KDA_DEV_BAD_SEQLENS);
+        return false;
+    }
+    return true;
+}
+
+// VEC consecutive elements as one access (VEC * sizeof(T) = 16 or 8 bytes, or one element).
+template <typename T, int VEC>
+struct Pack {
+    static constexpr int kWords = VEC * (int)sizeof(T) / 4 > 0 ? VEC * (int)sizeof(T) / 4 : 1;
+    uint32_t w[kWords];
+};
+template <int VEC, typename T>
+__device__ __forceinline__ Pack<T, VEC> load_pack(const T* p) {
+    Pack<T, VEC> r;
+    if constexpr (VEC * sizeof(T) == 16) {
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else if constexpr (VEC * sizeof(T) == 8) {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        r.w[0] = v.x; r.w[1] = v.y;
+    } else if constexpr (sizeof(T) == 2) {
+        static_assert(VEC == 1, "one element");
+        r.w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+    } else {
+        static_assert(VEC == 1, "one element");
+        r.w[0] = __ldg(reinterpret_cast<const unsigned int*>(p));
+    }
+    return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> zero_pack() {
+    Pack<T, VEC> r;
+#pragma unroll
+    for (int i = 0; i < Pack<T, VEC>::kWords; ++i) r.w[i] = 0;
+    return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack(const Pack<T, VEC>& p, float* f) {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) {
+        if constexpr (sizeof(T) == 2) {   // bf16 is the upper half of an fp32
+            f[i] = __uint_as_float((i & 1) ? (p.w[i / 2] & 0xffff0000u) : (p.w[i / 2] << 16));
+        } else {
+            f[i] = __uint_as_float(p.w[i]);
+        }
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> pack(const float* f) {
+    Pack<T, VEC> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) r.w[i] = __float_as_uint(f[i]);
+    } else if constexpr (VEC == 1) {
+        const __nv_bfloat16 h = __float2bfloat16_rn(f[0]);
+        r.w[0] = *reinterpret_cast<const unsigned short*>(&h);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            r.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
+    return r;
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_pack(T* p, const Pack<T, VEC>& v) {
+    if constexpr (VEC * sizeof(T) == 16) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    } else if constexpr (VEC * sizeof(T) == 8) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(v.w[0], v.w[1]);
+    } else if constexpr (sizeof(T) == 2) {
+        *reinterpret_cast<unsigned short*>(p) = (unsigned short)v.w[0];
+    } else {
+        *reinterpret_cast<unsigned int*>(p) = v.w[0];
+    }
+}
+template <typename T, int VEC>
+__device__ __forceinline__ void store_f32(T* p, const float* f) {
+    store_pack<T, VEC>(p, pack<T, VEC>(f));
+}
+
+// 1 / (1 + e^-v).  FAST (bf16 outputs): the hardware exponential and quotient, within a few
+// fp32 units, far below the output's rounding; otherwise the full-precision functions.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float v) {
+    if constexpr (FAST) return __fdividef(1.0f, 1.0f + __expf(-v));
+    return 1.0f / (1.0f + expf(-v));
+}
+
+// Whether every access of VEC * el bytes at p + k * stride_bytes is aligned.
+inline bool vec_ok(const void* p, long long stride_bytes, int bytes) {
+    return p == nullptr || ((reinterpret_cast<uintptr_t>(p) % (unsigned)bytes) == 0 && stride_bytes % bytes == 0);
+}
+
+}  // namespace kda

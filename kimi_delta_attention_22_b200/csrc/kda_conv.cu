@@ -1,0 +1,441 @@
+// kda_conv.cu -- short causal depthwise convolution with optional SiLU: forward over
+// rows, one-row step on a state of the last W - 1 inputs, gradients.
+//
+//   pre[t, d] = bias[d] + sum_j w[d, j] x[t - (W-1) + j, d],   out = pre sigmoid(pre)
+//   dpre = d_out sigmoid(pre) (1 + pre (1 - sigmoid(pre)))
+//   dx[s, d] = sum_j w[d, j] dpre[s + (W-1) - j, d],  dw[d, j] = sum_t dpre[t] x[t-(W-1)+j]
+//
+// Few operations per byte: HBM bounds every kernel here.  Every thread owns one access
+// of 16 (8) bytes of channels and walks a run of rows with the window of earlier inputs
+// in registers, so that each input is read once, plus W - 1 rows in front of each run.
+//
+// The tap count is a template parameter WM of {2, 3, 4, 8}; W = 5..7 run on WM = 8 with
+// the leading taps zero.  Taps are aligned at the newest input: tap WM - 1 is row t.
+#include "kda_block.cuh"
+
+namespace kda {
+namespace {
+
+template <int WM, int VEC>
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, int W, long long d0, float (*wr)[VEC],
+                                          float* br) {
+    if (WM == 4 && W == 4 && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {   // one 16-byte load per channel
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(w) + d0 + v);
+            const float t[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+            for (int j = 0; j < WM; ++j) wr[j][v] = t[j & 3];
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v)
+#pragma unroll
+            for (int j = 0; j < WM; ++j) {
+                const int jj = j - (WM - W);
+                wr[j][v] = jj >= 0 ? __ldg(w + (d0 + v) * W + jj) : 0.f;
+            }
+    }
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) br[v] = bias ? __ldg(bias + d0 + v) : 0.f;
+}
+
+// Inputs t - (WM-1) .. t - 1 of the sequence r (from its state in front of row r.b).
+template <typename T, int VEC, int WM>
+__device__ __forceinline__ void load_window(const ConvArgs& a, const SeqRange& r, long long t, long long d0,
+                                            Pack<T, VEC>* win) {
+    const T* x = static_cast<const T*>(a.x) + d0;
+    const T* st = static_cast<const T*>(a.state0);
+#pragma unroll
+    for (int j = 0; j < WM - 1; ++j) {
+        const long long p = t - (WM - 1) + j;
+        win[j] = zero_pack<T, VEC>();
+        if (p >= r.b) {
+            win[j] = load_pack<VEC>(x + p * a.xs);
+        } else if (st != nullptr) {
+            const int k = a.W - 1 + (int)(p - r.b);
+            if (k >= 0) win[j] = load_pack<VEC>(st + ((long long)r.q * (a.W - 1) + k) * a.D + d0);
+        }
+    }
+}
+
+template <typename T, int VEC, int WM>
+__device__ __forceinline__ void conv_pre(const Pack<T, VEC>* win, const Pack<T, VEC>& cur, const float (*wr)[VEC],
+                                         const float* br, float* pre) {
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) pre[v] = br[v];
+#pragma unroll
+    for (int j = 0; j < WM; ++j) {
+        float f[VEC];
+        unpack<T, VEC>(j < WM - 1 ? win[j < WM - 1 ? j : 0] : cur, f);
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) pre[v] = fmaf(wr[j][v], f[v], pre[v]);
+    }
+}
+
+template <typename T, int VEC, int WM, bool SILU>
+__global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int run, long long nruns) {
+    constexpr bool kFast = sizeof(T) == 2;
+    const int nvec = a.D / VEC;
+    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long d0 = (idx % nvec) * VEC;
+    const long long who = idx / nvec;
+    const T* x = static_cast<const T*>(a.x) + d0;
+    if (who >= nruns) {   // behind the runs: the final state of one sequence
+        const long long q = who - nruns;
+        long long b, e;
+        if (q >= a.num_seqs || !check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || a.stateT == nullptr) return;
+        const T* st = static_cast<const T*>(a.state0);
+        T* fin = static_cast<T*>(a.stateT);
+        for (int j = 0; j < a.W - 1; ++j) {
+            const long long p = e - (a.W - 1) + j;
+            Pack<T, VEC> v = zero_pack<T, VEC>();
+            if (p >= b) v = load_pack<VEC>(x + p * a.xs);
+            else if (st != nullptr) v = load_pack<VEC>(st + (q * (a.W - 1) + (a.W - 1) + (p - b)) * a.D + d0);
+            store_pack<T, VEC>(fin + (q * (a.W - 1) + j) * a.D + d0, v);
+        }
+        return;
+    }
+    float wr[WM][VEC], br[VEC];
+    load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
+    T* out = static_cast<T*>(a.out) + d0;
+    Pack<T, VEC> win[WM - 1];
+
+    long long t = who * run;
+    const long long t1 = t + run < a.M ? t + run : a.M;
+    auto emit = [&](long long row, const Pack<T, VEC>& cur) {
+        float pre[VEC];
+        conv_pre<T, VEC, WM>(win, cur, wr, br, pre);
+        if (SILU) {
+#pragma unroll
+            for (int v = 0; v < VEC; ++v) pre[v] *= sigmoid<kFast>(pre[v]);
+        }
+        store_f32<T, VEC>(out + row * a.D, pre);
+#pragma unroll
+        for (int j = 0; j + 1 < WM - 1; ++j) win[j] = win[j + 1];
+        win[WM - 2] = cur;
+    };
+    while (t < t1) {
+        const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, t);
+        if (!r.ok) { ++t; continue; }
+        const long long stop = t1 < r.e ? t1 : r.e;
+        load_window<T, VEC, WM>(a, r, t, d0, win);
+        constexpr int U = 4;
+        for (; t + U <= stop; t += U) {
+            Pack<T, VEC> nx[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) nx[u] = load_pack<VEC>(x + (t + u) * a.xs);
+#pragma unroll
+            for (int u = 0; u < U; ++u) emit(t + u, nx[u]);
+        }
+        for (; t < stop; ++t) emit(t, load_pack<VEC>(x + t * a.xs));
+    }
+}
+
+template <typename T, int VEC, int WM, bool SILU>
+__global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
+    const int nvec = a.D / VEC;
+    const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const long long n = idx / nvec, d0 = (idx % nvec) * VEC;
+    if (n >= a.num_seqs) return;
+    T* st = static_cast<T*>(a.stateT) + n * (a.W - 1) * a.D + d0;
+    Pack<T, VEC> win[WM - 1];
+#pragma unroll
+    for (int j = 0; j < WM - 1; ++j) {
+        const int k = j - (WM - a.W);
+        win[j] = zero_pack<T, VEC>();
+        if (k >= 0) win[j] = load_pack<VEC>(st + (long long)k * a.D);
+    }
+    const Pack<T, VEC> cur = load_pack<VEC>(static_cast<const T*>(a.x) + n * a.xs + d0);
+    float wr[WM][VEC], br[VEC], pre[VEC];
+    load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
+    conv_pre<T, VEC, WM>(win, cur, wr, br, pre);
+    if (SILU) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) pre[v] *= sigmoid<sizeof(T) == 2>(pre[v]);
+    }
+    store_f32<T, VEC>(static_cast<T*>(a.out) + n * a.D + d0, pre);
+#pragma unroll
+    for (int j = 1; j < WM - 1; ++j) {
+        const int k = j - 1 - (WM - a.W);
+        if (k >= 0) store_pack<T, VEC>(st + (long long)k * a.D, win[j]);
+    }
+    store_pack<T, VEC>(st + (long long)(a.W - 2) * a.D, cur);
+}
+
+// Backward.  A CTA owns 32 * VEC channels; its eight warps walk runs of rows and keep
+// their share of dw and db in registers, which are added over the warps at the end and
+// written as one partial sum per CTA.  A run needs dpre of up to WM - 1 rows behind it:
+// those are computed again (they belong to the next run's dw).
+constexpr int kBwdWarps = 8;
+
+template <typename T, typename TG, int VEC, int WM, bool SILU>
+__global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, int run, long long nruns, int K) {
+    constexpr bool kFast = sizeof(T) == 2;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const long long d0 = ((long long)blockIdx.x * 32 + lane) * VEC;
+    const bool live = d0 < a.D;
+    const T* x = static_cast<const T*>(a.x) + d0;
+    const TG* dy = static_cast<const TG*>(a.d_out) + d0;
+    T* dx = static_cast<T*>(a.dx) + d0;
+    float dw[WM][VEC] = {}, db[VEC] = {};
+    if (live) {
+        float wr[WM][VEC], br[VEC];
+        load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
+        const T* dfin = static_cast<const T*>(a.d_stateT);
+        T* dst = static_cast<T*>(a.dstate0);
+        for (long long rr = (long long)blockIdx.y * kBwdWarps + warp; rr < nruns; rr += (long long)K * kBwdWarps) {
+            long long p0 = rr * run;
+            const long long rend = p0 + run < a.M ? p0 + run : a.M;
+            while (p0 < rend) {
+                const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, p0);
+                if (!r.ok) { ++p0; continue; }
+                const long long p1 = rend < r.e ? rend : r.e;
+                Pack<T, VEC> win[WM - 1];
+                load_window<T, VEC, WM>(a, r, p0, d0, win);
+                float dp[WM][VEC] = {};   // dp[j] = dpre[t - j]
+                // row t enters; row s = t - (WM-1) has all of its gradients and leaves
+                auto leave = [&](long long t) {
+                    const long long s = t - (WM - 1);
+                    T* to;
+                    if (s >= p0) to = dx + s * a.D;
+                    else if (p0 == r.b && dst != nullptr && s - r.b >= -(a.W - 1))
+                        to = dst + ((long long)r.q * (a.W - 1) + (a.W - 1) + (s - r.b)) * a.D + d0;
+                    else return;
+                    float g[VEC] = {};
+                    const long long k = s - r.e + (a.W - 1);   // the row is the final state's k-th
+                    if (dfin != nullptr && k >= 0)
+                        unpack<T, VEC>(load_pack<VEC>(dfin + ((long long)r.q * (a.W - 1) + k) * a.D + d0), g);
+#pragma unroll
+                    for (int j = 0; j < WM; ++j)
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) g[v] = fmaf(wr[j][v], dp[j][v], g[v]);
+                    store_f32<T, VEC>(to, g);
+                };
+                auto enter = [&](const Pack<T, VEC>& cur, const Pack<TG, VEC>& gcur, bool mine) {
+                    float pre[VEC], g[VEC];
+                    unpack<TG, VEC>(gcur, g);
+                    if (SILU) {
+                        conv_pre<T, VEC, WM>(win, cur, wr, br, pre);
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) {
+                            const float sg = sigmoid<kFast>(pre[v]);
+                            g[v] *= sg * fmaf(pre[v], 1.0f - sg, 1.0f);
+                        }
+                    }
+#pragma unroll
+                    for (int j = WM - 1; j > 0; --j)
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) dp[j][v] = dp[j - 1][v];
+#pragma unroll
+                    for (int v = 0; v < VEC; ++v) dp[0][v] = g[v];
+                    if (mine) {
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) db[v] += g[v];
+#pragma unroll
+                        for (int j = 0; j < WM; ++j) {
+                            float f[VEC];
+                            unpack<T, VEC>(j < WM - 1 ? win[j < WM - 1 ? j : 0] : cur, f);
+#pragma unroll
+                            for (int v = 0; v < VEC; ++v) dw[j][v] = fmaf(g[v], f[v], dw[j][v]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j + 1 < WM - 1; ++j) win[j] = win[j + 1];
+                    win[WM - 2] = cur;
+                };
+                long long t = p0;
+                constexpr int U = 4;
+                for (; t + U <= p1; t += U) {
+                    Pack<T, VEC> nx[U];
+                    Pack<TG, VEC> ng[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        nx[u] = load_pack<VEC>(x + (t + u) * a.xs);
+                        ng[u] = load_pack<VEC>(dy + (t + u) * a.D);
+                    }
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        enter(nx[u], ng[u], true);
+                        leave(t + u);
+                    }
+                }
+                for (; t < p1; ++t) {
+                    enter(load_pack<VEC>(x + t * a.xs), load_pack<VEC>(dy + t * a.D), true);
+                    leave(t);
+                }
+                for (; t < p1 + WM - 1; ++t) {   // behind the piece: another run's rows, or past the sequence's end
+                    if (t < r.e) {
+                        enter(load_pack<VEC>(x + t * a.xs), load_pack<VEC>(dy + t * a.D), false);
+                    } else {
+#pragma unroll
+                        for (int j = WM - 1; j > 0; --j)
+#pragma unroll
+                            for (int v = 0; v < VEC; ++v) dp[j][v] = dp[j - 1][v];
+#pragma unroll
+                        for (int v = 0; v < VEC; ++v) dp[0][v] = 0.f;
+                    }
+                    leave(t);
+                }
+                p0 = p1;
+            }
+        }
+        // Sequences without rows hand their final state's gradient through; bounds are checked.
+        for (long long q = (long long)blockIdx.y * kBwdWarps + warp; q < a.num_seqs; q += (long long)K * kBwdWarps) {
+            long long b, e;
+            if (!check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || b != e || dst == nullptr) continue;
+            for (int j = 0; j < a.W - 1; ++j) {
+                Pack<T, VEC> v = zero_pack<T, VEC>();
+                if (dfin != nullptr) v = load_pack<VEC>(dfin + (q * (a.W - 1) + j) * a.D + d0);
+                store_pack<T, VEC>(dst + (q * (a.W - 1) + j) * a.D + d0, v);
+            }
+        }
+    }
+    extern __shared__ float red[];   // [kBwdWarps][WM + 1][VEC][32]
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) {
+#pragma unroll
+        for (int j = 0; j < WM; ++j) red[((warp * (WM + 1) + j) * VEC + v) * 32 + lane] = dw[j][v];
+        red[((warp * (WM + 1) + WM) * VEC + v) * 32 + lane] = db[v];
+    }
+    __syncthreads();
+    // part[blockIdx.y]: [D][W] of dw, then [D] of db
+    float* part = a.part + (long long)blockIdx.y * a.D * (a.W + 1);
+    for (int i = threadIdx.x; i < (WM + 1) * VEC * 32; i += blockDim.x) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kBwdWarps; ++w) s += red[w * (WM + 1) * VEC * 32 + i];
+        const int j = i / (VEC * 32), v = (i / 32) % VEC, l = i & 31;
+        const long long d = ((long long)blockIdx.x * 32 + l) * VEC + v;
+        if (d >= a.D) continue;
+        if (j == WM) part[(long long)a.D * a.W + d] = s;
+        else if (j >= WM - a.W) part[d * a.W + (j - (WM - a.W))] = s;
+    }
+}
+
+// Rows per thread of the forward: long runs re-read fewer halo rows (W - 1 per run),
+// short ones give more threads; as long as about 1024 threads per SM remain.
+int fwd_run(long long M, long long nvec) {
+    int run = 32;
+    while (run > 4 && nvec * ((M + run - 1) / run) < (long long)kSMs * 1024) run >>= 1;
+    return run;
+}
+
+struct BwdPlan {
+    int run, K;
+    long long nruns;
+};
+// Rows per run and CTAs along the rows (each writes one partial sum of dw and db).
+BwdPlan bwd_plan(long long M, int D, int vec) {
+    BwdPlan p;
+    const long long nblk = (D + 32LL * vec - 1) / (32LL * vec);
+    p.run = 64;
+    while (p.run > 8 && nblk * ((M + p.run - 1) / p.run) < (long long)kSMs * 16) p.run >>= 1;
+    p.nruns = (M + p.run - 1) / p.run;
+    long long K = (kSMs * 3 + nblk - 1) / nblk;
+    const long long most = (p.nruns + kBwdWarps - 1) / kBwdWarps;
+    if (K > most) K = most;
+    p.K = (int)(K < 1 ? 1 : K);
+    return p;
+}
+
+template <typename T, int VEC, bool SILU>
+cudaError_t fwd_w(const ConvArgs& a, cudaStream_t s) {
+    const long long nvec = a.D / VEC;
+    const int run = fwd_run(a.M, nvec);
+    const long long nruns = (a.M + run - 1) / run;
+    const long long grid = (nvec * (nruns + a.num_seqs) + 255) / 256;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    switch (a.W) {
+        case 2: conv_fwd_kernel<T, VEC, 2, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
+        case 3: conv_fwd_kernel<T, VEC, 3, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
+        case 4: conv_fwd_kernel<T, VEC, 4, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
+        default: conv_fwd_kernel<T, VEC, 8, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
+    }
+    return cudaGetLastError();
+}
+template <typename T, int VEC, bool SILU>
+cudaError_t step_w(const ConvArgs& a, cudaStream_t s) {
+    const long long grid = ((long long)(a.D / VEC) * a.num_seqs + 255) / 256;
+    if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    switch (a.W) {
+        case 2: conv_step_kernel<T, VEC, 2, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
+        case 3: conv_step_kernel<T, VEC, 3, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
+        case 4: conv_step_kernel<T, VEC, 4, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
+        default: conv_step_kernel<T, VEC, 8, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+template <typename T, typename TG, int VEC, int WM, bool SILU>
+cudaError_t bwd_one(const ConvArgs& a, cudaStream_t s) {
+    const BwdPlan p = bwd_plan(a.M, a.D, VEC);
+    const dim3 grid((unsigned)((a.D + 32 * VEC - 1) / (32 * VEC)), (unsigned)p.K);
+    const size_t smem = sizeof(float) * kBwdWarps * (WM + 1) * VEC * 32;
+    conv_bwd_kernel<T, TG, VEC, WM, SILU><<<grid, 32 * kBwdWarps, smem, s>>>(a, p.run, p.nruns, p.K);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_colsum(a.part, p.K, (long long)a.D * a.W, a.dw, a.D, a.db, 0, nullptr, s);
+}
+template <typename T, typename TG, int VEC, bool SILU>
+cudaError_t bwd_w(const ConvArgs& a, cudaStream_t s) {
+    switch (a.W) {
+        case 2: return bwd_one<T, TG, VEC, 2, SILU>(a, s);
+        case 3: return bwd_one<T, TG, VEC, 3, SILU>(a, s);
+        case 4: return bwd_one<T, TG, VEC, 4, SILU>(a, s);
+        default: return bwd_one<T, TG, VEC, 8, SILU>(a, s);
+    }
+}
+template <typename T, typename TG, int VEC>
+cudaError_t bwd_act(const ConvArgs& a, bool silu, cudaStream_t s) {
+    return silu ? bwd_w<T, TG, VEC, true>(a, s) : bwd_w<T, TG, VEC, false>(a, s);
+}
+
+// 16-byte (forward, step) or 8-byte (bf16 backward) accesses need every row of every
+// tensor to start on such a boundary.
+bool rows_ok(const ConvArgs& a, int el, int vec) {
+    const int by = el * vec;
+    const long long row = (long long)a.D * el;
+    return a.D % vec == 0 && vec_ok(a.x, a.xs * el, by) && vec_ok(a.out, row, by) && vec_ok(a.state0, row, by) &&
+           vec_ok(a.stateT, row, by) && vec_ok(a.dx, row, by) && vec_ok(a.dstate0, row, by) &&
+           vec_ok(a.d_stateT, row, by);
+}
+
+template <typename T>
+cudaError_t fwd_t(const ConvArgs& a, bool silu, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (rows_ok(a, sizeof(T), V)) return silu ? fwd_w<T, V, true>(a, s) : fwd_w<T, V, false>(a, s);
+    return silu ? fwd_w<T, 1, true>(a, s) : fwd_w<T, 1, false>(a, s);
+}
+template <typename T>
+cudaError_t step_t(const ConvArgs& a, bool silu, cudaStream_t s) {
+    constexpr int V = 16 / sizeof(T);
+    if (rows_ok(a, sizeof(T), V)) return silu ? step_w<T, V, true>(a, s) : step_w<T, V, false>(a, s);
+    return silu ? step_w<T, 1, true>(a, s) : step_w<T, 1, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_conv_fwd(const ConvArgs& a, bool bf16, bool silu, cudaStream_t s) {
+    return bf16 ? fwd_t<__nv_bfloat16>(a, silu, s) : fwd_t<float>(a, silu, s);
+}
+
+cudaError_t launch_conv_step(const ConvArgs& a, bool bf16, bool silu, cudaStream_t s) {
+    return bf16 ? step_t<__nv_bfloat16>(a, silu, s) : step_t<float>(a, silu, s);
+}
+
+size_t conv_bwd_workspace_bytes(long long M, int D, int W) {
+    const int k4 = bwd_plan(M, D, 4).K, k1 = bwd_plan(M, D, 1).K;
+    return sizeof(float) * (size_t)(k4 > k1 ? k4 : k1) * D * (W + 1);
+}
+
+cudaError_t launch_conv_bwd(const ConvArgs& a, bool bf16, bool grad_bf16, bool silu, cudaStream_t s) {
+    const int el = bf16 ? 2 : 4, gel = grad_bf16 ? 2 : 4;
+    const bool vec = rows_ok(a, el, 4) && vec_ok(a.d_out, (long long)a.D * gel, 4 * gel);
+    if (!bf16) return vec ? bwd_act<float, float, 4>(a, silu, s) : bwd_act<float, float, 1>(a, silu, s);
+    if (grad_bf16)
+        return vec ? bwd_act<__nv_bfloat16, __nv_bfloat16, 4>(a, silu, s)
+                   : bwd_act<__nv_bfloat16, __nv_bfloat16, 1>(a, silu, s);
+    return vec ? bwd_act<__nv_bfloat16, float, 4>(a, silu, s) : bwd_act<__nv_bfloat16, float, 1>(a, silu, s);
+}
+
+}  // namespace kda

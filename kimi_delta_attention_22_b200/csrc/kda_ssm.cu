@@ -1,0 +1,431 @@
+// kda_ssm.cu -- selective state space scan: forward over rows, and one row on a state.
+//
+//   dt = softplus(delta + bias),  h[n] <- e^{dt A[n]} h[n] + dt x B[n]
+//   y = sum_n h[n] C[n] + Dskip x,  out = y silu(z)
+//
+// Per row and channel: N exponentials (they depend on the row, the channel and the state,
+// so no product of matrices holds them) and about 4 N fp32 operations.  The special-function
+// unit gives 16 exponentials per cycle and SM, which bounds the scan; the bytes (x, delta, z,
+// out, once each) take about a third of that time at N = 16.
+//
+// A CTA of 128 threads owns 128 / S channels of one group: S lanes per channel, NS states per
+// lane in registers for all rows.  Rows come in tiles: every thread holds the next tile's x,
+// delta and z of one row and eight channels in registers (loaded while the current tile is
+// scanned), forms dt and dt x in fp32 and lays them down in shared memory [channel][row],
+// where the scan reads four rows at a time; B and C are laid down once per tile for all
+// channels.  The sum over a channel's lanes is taken for four rows at once (the lanes swap
+// halves, so that two exchanges and one more serve four sums).  y goes back through shared
+// memory to the thread that holds the row's x and z.
+//
+// Too few channels and sequences to fill the SMs: the rows are cut into segments, aligned to
+// the row index and not to sequences.  Pass 1 scans every segment from zero (keeping only the
+// last state and the sum of dt), a short pass joins them (the decay over a segment is
+// e^{A sum dt}), pass 2 scans again from the right state.  This doubles the exponentials, so
+// it is used only below one CTA per SM.
+#include "kda_ssm.cuh"
+
+namespace kda {
+namespace ssm {
+namespace {
+
+constexpr int kThreads = 128;
+
+template <int S>
+constexpr int tile_rows() { return S >= 4 ? 32 : 8 * S; }
+
+template <typename T, int S, int NS, bool ALIGNED, bool SUMMARY>
+__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(SsmArgs a, Segments seg, int nblk, float* hseg, float* dtseg) {
+    constexpr int CH = kThreads / S, TT = tile_rows<S>(), LD = TT + 4, NP = S * NS;
+    constexpr int VPR = CH / 8;                 // threads per staged row
+    constexpr int BPT = (TT * NP + kThreads - 1) / kThreads;   // staged elements of B (and C) per thread
+    constexpr bool kAhead = BPT <= 8;           // B and C of the next tile wait in registers
+    static_assert(TT * VPR <= kThreads && TT % 4 == 0, "tile");
+    __shared__ __align__(16) float s_dt[CH * LD];
+    __shared__ __align__(16) float s_u[CH * LD];
+    __shared__ __align__(16) float s_y[SUMMARY ? 4 : CH * LD];
+    __shared__ __align__(16) float s_B[TT * NP];
+    __shared__ __align__(16) float s_C[SUMMARY ? 4 : TT * NP];
+
+    const long long sg = blockIdx.x / nblk;   // segment, or behind them
+    const ChannelBlock cb = channel_block<CH>(blockIdx.x % nblk, a.D, a.G);
+    const int tid = threadIdx.x, ch = tid / S, s = tid % S;
+    const bool live = ch < cb.n;
+    const int d = cb.d0 + (live ? ch : 0);
+
+    if (!SUMMARY && sg >= seg.count) {
+        // behind the segments: sequences without rows hand their state through, bounds are checked
+        for (long long q = sg - seg.count; q < a.num_seqs; q += gridDim.x / nblk - seg.count) {
+            long long b, e;
+            if (!check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || b != e || a.hT == nullptr || !live) continue;
+            const long long at = (q * a.D + d) * a.N;
+            for (int n = s * NS; n < s * NS + NS && n < a.N; ++n) a.hT[at + n] = a.h0 ? a.h0[at + n] : 0.f;
+        }
+        return;
+    }
+
+    const long long t0 = sg * seg.len;
+    const long long t1 = t0 + seg.len < a.M ? t0 + seg.len : a.M;
+    float A2[NS], h[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int n = s * NS + i;
+        A2[i] = live && n < a.N ? a.A[(long long)d * a.N + n] * kLog2e : 0.f;
+        h[i] = 0.f;
+        if (!SUMMARY && !seg.whole && live && n < a.N)
+            h[i] = hseg[(sg * a.D + d) * a.N + n];   // used unless a sequence starts at t0
+    }
+    float dtsum = 0.f;
+
+    // staging: this thread's row of the tile and its eight channels
+    const int srow = tid / VPR, sc0 = (tid % VPR) * 8;
+    const bool stager = tid < TT * VPR;
+    const int scn = stager ? max(0, min(8, cb.n - sc0)) : 0;
+    const int sd = cb.d0 + sc0;
+    const T* xp = static_cast<const T*>(a.x) + sd;
+    const T* dp = static_cast<const T*>(a.delta) + sd;
+    const T* zp = static_cast<const T*>(a.z) + sd;
+    const T* Bp = static_cast<const T*>(a.Bm) + (long long)cb.g * a.N;
+    const T* Cp = static_cast<const T*>(a.Cm) + (long long)cb.g * a.N;
+    float bias[8], dsk[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        bias[i] = i < scn && a.delta_bias ? a.delta_bias[sd + i] : 0.f;
+        dsk[i] = i < scn && a.Dskip ? a.Dskip[sd + i] : 0.f;
+    }
+    Pack<T, 8> nx, nd, nz;
+    float nB[kAhead ? BPT : 1], nC[kAhead ? BPT : 1];
+    auto bc = [&](const T* p, long long stride, long long tile, int e) {   // element e of this thread's share
+        const int k = e * kThreads + tid, row = k / NP, n = k % NP;
+        return row < TT && tile + row < t1 && n < a.N ? to_f32<T>(p[(tile + row) * stride + n]) : 0.f;
+    };
+    auto fetch = [&](long long tile) {
+        const long long t = tile + srow;
+        const int n = t < t1 ? scn : 0;
+        nx = load8<T, ALIGNED>(xp + t * a.xs, n);
+        nd = load8<T, ALIGNED>(dp + t * a.ds, n);
+        if (!SUMMARY) nz = a.z ? load8<T, ALIGNED>(zp + t * a.zs, n) : zero_pack<T, 8>();
+        if constexpr (kAhead) {
+#pragma unroll
+            for (int e = 0; e < BPT; ++e) {
+                nB[e] = bc(Bp, a.bs, tile, e);
+                if (!SUMMARY) nC[e] = bc(Cp, a.cs, tile, e);
+            }
+        }
+    };
+
+    SeqRange r{0, 0, 0, false};
+    auto enter = [&](long long t) {   // row t is the first one, or the first behind r
+        r = find_seq(a.cu, a.num_seqs, a.M, a.T, t);
+        if (r.ok && r.b == t) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int n = s * NS + i;
+                h[i] = a.h0 && live && n < a.N ? a.h0[((long long)r.q * a.D + d) * a.N + n] : 0.f;
+            }
+        }
+    };
+    auto finish = [&]() {   // the state is that of r's last row
+        if constexpr (!SUMMARY) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int n = s * NS + i;
+                if (a.hT != nullptr && live && n < a.N) a.hT[((long long)r.q * a.D + d) * a.N + n] = h[i];
+            }
+        }
+    };
+    auto row_step = [&](float dt, float u, int i) {   // one row of the tile; the lane's share of y
+        float y = 0.f;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+            h[j] = fmaf(ex2(dt * A2[j]), h[j], u * s_B[i * NP + s * NS + j]);
+            if (!SUMMARY) y = fmaf(h[j], s_C[i * NP + s * NS + j], y);
+        }
+        if (SUMMARY) dtsum += dt;
+        return y;
+    };
+
+    fetch(t0);
+    for (long long tile = t0; tile < t1; tile += TT) {
+        const Pack<T, 8> cx = nx, cz = nz;
+        if (stager) {
+            float x[8], v[8];
+            unpack<T, 8>(nx, x);
+            unpack<T, 8>(nd, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] += bias[i];
+                if (a.softplus) v[i] = softplus(v[i]);
+                s_dt[(sc0 + i) * LD + srow] = v[i];
+                s_u[(sc0 + i) * LD + srow] = v[i] * x[i];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < BPT; ++e) {
+            if (e * kThreads + tid >= TT * NP) continue;
+            if constexpr (kAhead) {
+                s_B[e * kThreads + tid] = nB[e];
+                if (!SUMMARY) s_C[e * kThreads + tid] = nC[e];
+            } else {
+                s_B[e * kThreads + tid] = bc(Bp, a.bs, tile, e);
+                if (!SUMMARY) s_C[e * kThreads + tid] = bc(Cp, a.cs, tile, e);
+            }
+        }
+        __syncthreads();
+        if (tile + TT < t1) fetch(tile + TT);
+        const int rows = (int)(t1 - tile < TT ? t1 - tile : TT);
+        if (!r.ok || tile >= r.e) enter(tile);
+        const bool whole = rows == TT && r.ok && tile + TT <= r.e;   // the tile lies in one sequence
+        if (whole) {
+#pragma unroll 2
+            for (int i = 0; i < TT; i += 4) {
+                const float4 d4 = *reinterpret_cast<const float4*>(&s_dt[ch * LD + i]);
+                const float4 u4 = *reinterpret_cast<const float4*>(&s_u[ch * LD + i]);
+                const float y0 = row_step(d4.x, u4.x, i);
+                const float y1 = row_step(d4.y, u4.y, i + 1);
+                const float y2 = row_step(d4.z, u4.z, i + 2);
+                const float y3 = row_step(d4.w, u4.w, i + 3);
+                if constexpr (!SUMMARY) lane_sum4<S>(y0, y1, y2, y3, s, &s_y[ch * LD + i]);
+            }
+            if (tile + TT == r.e) finish();
+        } else {
+            for (int i = 0; i < rows; ++i) {
+                if (!r.ok || tile + i >= r.e) enter(tile + i);
+                if (!r.ok) continue;   // a row of no sequence
+                float y = row_step(s_dt[ch * LD + i], s_u[ch * LD + i], i);
+                if (!SUMMARY) {
+#pragma unroll
+                    for (int m = 1; m < S; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+                    if (s == 0) s_y[ch * LD + i] = y;
+                }
+                if (tile + i + 1 == r.e) finish();
+            }
+        }
+        __syncthreads();
+        if (!SUMMARY && stager && tile + srow < t1) {
+            if (whole || a.cu == nullptr || find_seq(a.cu, a.num_seqs, a.M, a.T, tile + srow).ok) {
+                float x[8], z[8], y[8];
+                unpack<T, 8>(cx, x);
+                unpack<T, 8>(cz, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = fmaf(dsk[i], x[i], s_y[(sc0 + i) * LD + srow]);
+                    if (a.z) y[i] *= z[i] * sigmoid<sizeof(T) == 2>(z[i]);
+                }
+                store8<T, ALIGNED>(static_cast<T*>(a.out) + (tile + srow) * a.D + sd, y, scn);
+            }
+        }
+    }
+    if (SUMMARY && live) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int n = s * NS + i;
+            if (n < a.N) hseg[(sg * a.D + d) * a.N + n] = h[i];
+        }
+        if (s == 0) dtseg[sg * a.D + d] = dtsum;
+    }
+}
+
+// hseg[k] (the state that segment k alone ends with) -> the state that enters segment k.
+__global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a, Segments seg, float* hseg, const float* dtseg) {
+    extern __shared__ uint8_t s_new[];
+    for (long long k = threadIdx.x; k < seg.count; k += blockDim.x) {
+        const long long t0 = k * seg.len, t1 = t0 + seg.len < a.M ? t0 + seg.len : a.M;
+        s_new[k] = starts_inside(a, t0, t1);
+    }
+    __syncthreads();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, DN = (long long)a.D * a.N;
+    if (i >= DN) return;
+    const float A2 = a.A[i] * kLog2e;
+    const long long d = i / a.N;
+    float h = 0.f;
+#pragma unroll 4
+    for (long long k = 0; k < seg.count; ++k) {
+        const float own = hseg[k * DN + i], dt = dtseg[k * a.D + d];
+        hseg[k * DN + i] = h;
+        h = s_new[k] ? own : fmaf(ex2(dt * A2), h, own);
+    }
+}
+
+// One row of every sequence: the fp32 state is read and written once, which bounds the step.
+// S lanes per channel, four states per lane (one 16-byte access where N is a multiple of 4);
+// a thread takes the same channel of up to four sequences, their loads first.
+template <typename T, int S, bool VEC4>
+__global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
+    constexpr int NB = 4;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    const int s = (int)(i % S);
+    const bool live = i / S < a.D;
+    const int d = live ? (int)(i / S) : 0;
+    const int n0 = s * 4, g = d / (a.D / a.G);
+    const long long q0 = (long long)blockIdx.y * NB;
+    float A2[4], h[NB][4], B[NB][4], C[NB][4], x[NB], v[NB], z[NB];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const long long q = q0 + b;
+        const bool on = live && q < a.num_seqs;
+        x[b] = on ? to_f32<T>(static_cast<const T*>(a.x)[q * a.xs + d]) : 0.f;
+        v[b] = on ? to_f32<T>(static_cast<const T*>(a.delta)[q * a.ds + d]) : 0.f;
+        z[b] = on && a.z ? to_f32<T>(static_cast<const T*>(a.z)[q * a.zs + d]) : 0.f;
+        const float* hp = a.hT + (q * a.D + d) * a.N + n0;
+        const T* Bp = static_cast<const T*>(a.Bm) + q * a.bs + (long long)g * a.N + n0;
+        const T* Cp = static_cast<const T*>(a.Cm) + q * a.cs + (long long)g * a.N + n0;
+        if (VEC4) {
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            const bool in = on && n0 < a.N;
+            if (in) f = *reinterpret_cast<const float4*>(hp);
+            h[b][0] = f.x; h[b][1] = f.y; h[b][2] = f.z; h[b][3] = f.w;
+            unpack<T, 4>(in ? load_pack<4>(Bp) : zero_pack<T, 4>(), B[b]);
+            unpack<T, 4>(in ? load_pack<4>(Cp) : zero_pack<T, 4>(), C[b]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = on && n0 + j < a.N;
+                h[b][j] = in ? hp[j] : 0.f;
+                B[b][j] = in ? to_f32<T>(Bp[j]) : 0.f;
+                C[b][j] = in ? to_f32<T>(Cp[j]) : 0.f;
+            }
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) A2[j] = live && n0 + j < a.N ? a.A[(long long)d * a.N + n0 + j] * kLog2e : 0.f;
+    const float bias = a.delta_bias && live ? a.delta_bias[d] : 0.f;
+    const float dsk = a.Dskip && live ? a.Dskip[d] : 0.f;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        const long long q = q0 + b;
+        const bool on = live && q < a.num_seqs;
+        float dt = v[b] + bias;
+        if (a.softplus) dt = softplus(dt);
+        const float u = dt * x[b];
+        float y = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            h[b][j] = fmaf(ex2(dt * A2[j]), h[b][j], u * B[b][j]);
+            y = fmaf(h[b][j], C[b][j], y);
+        }
+#pragma unroll
+        for (int m = 1; m < S; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
+        if (!on) continue;
+        float* hp = a.hT + (q * a.D + d) * a.N + n0;
+        if (VEC4) {
+            if (n0 < a.N) *reinterpret_cast<float4*>(hp) = make_float4(h[b][0], h[b][1], h[b][2], h[b][3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (n0 + j < a.N) hp[j] = h[b][j];
+        }
+        if (s == 0) {
+            y = fmaf(dsk, x[b], y);
+            if (a.z) y *= z[b] * sigmoid<sizeof(T) == 2>(z[b]);
+            static_cast<T*>(a.out)[q * a.D + d] = from_f32<T>(y);
+        }
+    }
+}
+
+// Lanes per channel for N states (four, or eight states per lane above 32).
+int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 64 ? 8 : 16; }
+int tile_for(int N) {
+    const int S = lanes_for(N);
+    return S >= 4 ? 32 : 8 * S;
+}
+
+// One segment per sequence of a dense batch (all rows of a packed one) as soon as that gives
+// a CTA per SM: cutting the rows costs a second set of exponentials.
+Segments plan(long long B, long long T, int D, int N, int G, bool varlen) {
+    const long long M = B * T, whole = varlen ? 1 : B;
+    const long long blocks = channel_blocks(D, G, kThreads / lanes_for(N));
+    Segments p{varlen ? M : T, whole, true};
+    if (blocks * whole >= kSMs) return p;
+    long long count = (4LL * kSMs + blocks - 1) / blocks;
+    const long long most = M / 128;   // at least 128 rows each
+    if (count > most) count = most;
+    if (count > 1024) count = 1024;
+    if (count <= 2 * whole) return p;   // at most twice the CTAs for twice the work
+    const int tile = tile_for(N);
+    p.len = ((M + count - 1) / count + tile - 1) / tile * tile;
+    p.count = (M + p.len - 1) / p.len;
+    p.whole = false;
+    return p;
+}
+
+template <typename T, int S, int NS, bool ALIGNED>
+cudaError_t fwd_go(const SsmArgs& a, const Segments& p, cudaStream_t s) {
+    const long long blocks = channel_blocks(a.D, a.G, kThreads / S);
+    // sequences without rows (packed, or T = 0) are served behind the segments
+    const long long extra = a.cu != nullptr || a.T == 0 ? (a.num_seqs < 64 ? a.num_seqs : 64) : 0;
+    if (blocks * (p.count + extra) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    if (p.count + extra == 0) return cudaSuccess;
+    const int nblk = (int)blocks;
+    float* hseg = reinterpret_cast<float*>(a.ws);
+    float* dtseg = hseg + p.count * a.D * a.N;
+    if (!p.whole) {
+        ssm_scan_kernel<T, S, NS, ALIGNED, true>
+            <<<(unsigned)(blocks * p.count), kThreads, 0, s>>>(a, p, nblk, hseg, dtseg);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        const long long dn = (long long)a.D * a.N;
+        ssm_join_kernel<<<(unsigned)((dn + 127) / 128), 128, (size_t)p.count, s>>>(a, p, hseg, dtseg);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    ssm_scan_kernel<T, S, NS, ALIGNED, false>
+        <<<(unsigned)(blocks * (p.count + extra)), kThreads, 0, s>>>(a, p, nblk, hseg, dtseg);
+    return cudaGetLastError();
+}
+
+template <typename T, bool ALIGNED>
+cudaError_t fwd_n(const SsmArgs& a, const Segments& p, cudaStream_t s) {
+    if (a.N <= 4) return fwd_go<T, 1, 4, ALIGNED>(a, p, s);
+    if (a.N <= 8) return fwd_go<T, 2, 4, ALIGNED>(a, p, s);
+    if (a.N <= 16) return fwd_go<T, 4, 4, ALIGNED>(a, p, s);
+    if (a.N <= 32) return fwd_go<T, 8, 4, ALIGNED>(a, p, s);
+    if (a.N <= 64) return fwd_go<T, 8, 8, ALIGNED>(a, p, s);
+    return fwd_go<T, 16, 8, ALIGNED>(a, p, s);
+}
+
+template <typename T>
+cudaError_t fwd_t(const SsmArgs& a, cudaStream_t s) {
+    const int el = sizeof(T);
+    const Segments p = plan(a.T > 0 ? a.M / a.T : 0, a.T, a.D, a.N, a.G, a.cu != nullptr);
+    const bool al = (a.D / a.G) % 8 == 0 && vec_ok(a.x, a.xs * el, 16) && vec_ok(a.delta, a.ds * el, 16) &&
+                    vec_ok(a.z, a.zs * el, 16) && vec_ok(a.out, (long long)a.D * el, 16);
+    return al ? fwd_n<T, true>(a, p, s) : fwd_n<T, false>(a, p, s);
+}
+
+template <typename T, bool VEC4>
+cudaError_t step_n(const SsmArgs& a, cudaStream_t s) {
+    const int S = a.N <= 4 ? 1 : a.N <= 8 ? 2 : a.N <= 16 ? 4 : a.N <= 32 ? 8 : a.N <= 64 ? 16 : 32;
+    const long long gx = ((long long)a.D * S + 255) / 256, gy = (a.num_seqs + 3) / 4;
+    if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidConfiguration;
+    const dim3 grid((unsigned)gx, (unsigned)gy);
+    switch (S) {
+        case 1: ssm_step_kernel<T, 1, VEC4><<<grid, 256, 0, s>>>(a); break;
+        case 2: ssm_step_kernel<T, 2, VEC4><<<grid, 256, 0, s>>>(a); break;
+        case 4: ssm_step_kernel<T, 4, VEC4><<<grid, 256, 0, s>>>(a); break;
+        case 8: ssm_step_kernel<T, 8, VEC4><<<grid, 256, 0, s>>>(a); break;
+        case 16: ssm_step_kernel<T, 16, VEC4><<<grid, 256, 0, s>>>(a); break;
+        default: ssm_step_kernel<T, 32, VEC4><<<grid, 256, 0, s>>>(a); break;
+    }
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace ssm
+
+cudaError_t launch_ssm_fwd(const SsmArgs& a, bool bf16, cudaStream_t s) {
+    return bf16 ? ssm::fwd_t<__nv_bfloat16>(a, s) : ssm::fwd_t<float>(a, s);
+}
+
+size_t ssm_fwd_workspace_bytes(long long B, long long T, int D, int N, int G, bool varlen) {
+    const ssm::Segments p = ssm::plan(B, T, D, N, G, varlen);
+    return p.whole ? 0 : sizeof(float) * (size_t)p.count * D * (N + 1);
+}
+
+cudaError_t launch_ssm_step(const SsmArgs& a, bool bf16, cudaStream_t s) {
+    const int b4 = bf16 ? 8 : 16, el = b4 / 4;   // four states at a time
+    const bool v = a.N % 4 == 0 && vec_ok(a.hT, 16, 16) && vec_ok(a.Bm, a.bs * el, b4) && vec_ok(a.Cm, a.cs * el, b4);
+    if (bf16) return v ? ssm::step_n<__nv_bfloat16, true>(a, s) : ssm::step_n<__nv_bfloat16, false>(a, s);
+    return v ? ssm::step_n<float, true>(a, s) : ssm::step_n<float, false>(a, s);
+}
+
+}  // namespace kda

@@ -1,0 +1,141 @@
+// kda_ssm.cuh -- device pieces that the selective scan's forward, step and gradient share.
+#pragma once
+
+#include "kda_block.cuh"
+
+namespace kda {
+namespace ssm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// softplus(v) = max(v, 0) + log(1 + e), e = e^-|v| <= 1.  With s = e / (2 + e) <= 1/3,
+// log(1 + e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ..): the series ends at s^14/15, whose
+// remainder is below 2e-9 of the sum, so the value keeps its relative accuracy where e is
+// tiny (step sizes of 1e-3 and less), which a logarithm of 1 + e does not.
+__device__ __forceinline__ float softplus(float v) {
+    const float e = ex2(-kLog2e * fabsf(v));
+    const float s = __fdividef(e, 2.0f + e), q = s * s;
+    float p = 1.0f / 15.0f;
+    p = fmaf(p, q, 1.0f / 13.0f);
+    p = fmaf(p, q, 1.0f / 11.0f);
+    p = fmaf(p, q, 1.0f / 9.0f);
+    p = fmaf(p, q, 1.0f / 7.0f);
+    p = fmaf(p, q, 1.0f / 5.0f);
+    p = fmaf(p, q, 1.0f / 3.0f);
+    p = fmaf(p, q, 1.0f);
+    return fmaf(2.0f * s, p, fmaxf(v, 0.0f));   // a NaN stays one through e
+}
+
+// 8 consecutive channels of one row (those below `n`), as raw words.
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ Pack<T, 8> load8(const T* p, int n) {
+    Pack<T, 8> r = zero_pack<T, 8>();
+    if constexpr (ALIGNED) {
+        if (n > 0) {
+            if constexpr (sizeof(T) == 2) {
+                r = load_pack<8>(p);
+            } else {
+                const Pack<T, 4> a = load_pack<4>(p), b = load_pack<4>(p + 4);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    r.w[i] = a.w[i];
+                    r.w[4 + i] = b.w[i];
+                }
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) {
+                const uint32_t w = load_pack<1>(p + i).w[0];
+                if constexpr (sizeof(T) == 2) r.w[i / 2] |= w << (16 * (i & 1));
+                else r.w[i] = w;
+            }
+    }
+    return r;
+}
+template <typename T, bool ALIGNED>
+__device__ __forceinline__ void store8(T* p, const float* f, int n) {
+    if constexpr (ALIGNED) {
+        if (n > 0) {
+            if constexpr (sizeof(T) == 2) {
+                store_f32<T, 8>(p, f);
+            } else {
+                store_f32<T, 4>(p, f);
+                store_f32<T, 4>(p + 4, f + 4);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) store_f32<T, 1>(p + i, f + i);
+    }
+}
+
+// Where a CTA's channels lie: CH consecutive channels of one group.
+struct ChannelBlock {
+    int d0, n, g;   // first channel, channels (<= CH), group
+};
+template <int CH>
+__device__ __forceinline__ ChannelBlock channel_block(int blk, int D, int G) {
+    const int dg = D / G, per = (dg + CH - 1) / CH;
+    ChannelBlock c;
+    c.g = blk / per;
+    const int off = (blk - c.g * per) * CH;
+    c.d0 = c.g * dg + off;
+    c.n = dg - off < CH ? dg - off : CH;
+    return c;
+}
+inline long long channel_blocks(int D, int G, int CH) { return (long long)G * ((D / G + CH - 1) / CH); }
+
+// The sums over a channel's S lanes (lane s of them) of four rows' values, written to
+// to[0..3]: lanes swap the halves that they do not keep, so that after two exchanges lane
+// s & 3 holds its row, and the remaining lanes are added in full.
+template <int S>
+__device__ __forceinline__ void lane_sum4(float y0, float y1, float y2, float y3, int s, float* to) {
+    if constexpr (S >= 2) {   // lanes with bit 0 keep rows 1 and 3
+        const bool up = s & 1;
+        const float k0 = up ? y1 : y0, k1 = up ? y3 : y2;
+        y0 = k0 + __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 1);
+        y1 = k1 + __shfl_xor_sync(0xffffffffu, up ? y2 : y3, 1);
+    }
+    if constexpr (S >= 4) {   // lanes with bit 1 keep rows 2 and 3
+        const bool up = s & 2;
+        const float k0 = up ? y1 : y0;
+        y0 = k0 + __shfl_xor_sync(0xffffffffu, up ? y0 : y1, 2);
+    }
+#pragma unroll
+    for (int m = 4; m < S; m <<= 1) y0 += __shfl_xor_sync(0xffffffffu, y0, m);
+    if constexpr (S == 1) {
+        *reinterpret_cast<float4*>(to) = make_float4(y0, y1, y2, y3);
+    } else if constexpr (S == 2) {
+        to[s] = y0;
+        to[2 + s] = y1;
+    } else {
+        if (s < 4) to[s] = y0;
+    }
+}
+
+// Rows of the segments that the long axis is cut into (a multiple of the tile's rows), and
+// how many; `whole`: one segment is exactly one sequence of a dense batch (or all rows), so
+// that no segment starts inside a sequence.
+struct Segments {
+    long long len, count;
+    bool whole;
+};
+
+// Whether segment [t0, t1) holds the first row of a sequence: its outgoing state then does
+// not depend on its incoming one.  Rows in no sequence count as such.
+__device__ __forceinline__ bool starts_inside(const SsmArgs& a, long long t0, long long t1) {
+    const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, t1 - 1);
+    return !r.ok || r.b >= t0;
+}
+
+}  // namespace ssm
+}  // namespace kda
