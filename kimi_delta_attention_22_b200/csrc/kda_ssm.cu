@@ -33,27 +33,40 @@ constexpr int kThreads = 128;
 template <int S>
 constexpr int tile_rows() { return S >= 4 ? 32 : 8 * S; }
 
+// Named barriers between the scanning and the staging warps: FULL + b, tile buffer b holds a
+// tile; DONE + b, its scan has ended (y lies in s_y[b], the inputs may be overwritten).
+enum { kFull = 1, kDone = 3 };
+template <int ID>
+__device__ __forceinline__ void bar_sync(int b) {   // the id is an immediate: the CTA then holds 5 barriers, not all 16
+    if (b == 0) asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(2 * kThreads) : "memory");
+    else asm volatile("bar.sync %0, %1;" ::"n"(ID + 1), "n"(2 * kThreads) : "memory");
+}
+template <int ID>
+__device__ __forceinline__ void bar_arrive(int b) {
+    if (b == 0) asm volatile("bar.arrive %0, %1;" ::"n"(ID), "n"(2 * kThreads) : "memory");
+    else asm volatile("bar.arrive %0, %1;" ::"n"(ID + 1), "n"(2 * kThreads) : "memory");
+}
+
 template <typename T, int S, int NS, bool ALIGNED, bool SUMMARY>
-__global__ void __launch_bounds__(kThreads) ssm_scan_kernel(SsmArgs a, Segments seg, int nblk, float* hseg, float* dtseg) {
+__global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Segments seg, int nblk, float* hseg, float* dtseg) {
     constexpr int CH = kThreads / S, TT = tile_rows<S>(), LD = TT + 4, NP = S * NS;
     constexpr int VPR = CH / 8;                 // threads per staged row
     constexpr int BPT = (TT * NP + kThreads - 1) / kThreads;   // staged elements of B (and C) per thread
     constexpr bool kAhead = BPT <= 8;           // B and C of the next tile wait in registers
     static_assert(TT * VPR <= kThreads && TT % 4 == 0, "tile");
-    __shared__ __align__(16) float s_dt[CH * LD];
-    __shared__ __align__(16) float s_u[CH * LD];
-    __shared__ __align__(16) float s_y[SUMMARY ? 4 : CH * LD];
-    __shared__ __align__(16) float s_B[TT * NP];
-    __shared__ __align__(16) float s_C[SUMMARY ? 4 : TT * NP];
+    extern __shared__ __align__(16) float sm[];   // two tile buffers
+    constexpr int kBuf = (SUMMARY ? 2 : 3) * CH * LD + (SUMMARY ? 1 : 2) * TT * NP;
 
     const long long sg = blockIdx.x / nblk;   // segment, or behind them
     const ChannelBlock cb = channel_block<CH>(blockIdx.x % nblk, a.D, a.G);
-    const int tid = threadIdx.x, ch = tid / S, s = tid % S;
+    const bool scanner = threadIdx.x < kThreads;
+    const int tid = threadIdx.x & (kThreads - 1), ch = tid / S, s = tid % S;
     const bool live = ch < cb.n;
     const int d = cb.d0 + (live ? ch : 0);
 
     if (!SUMMARY && sg >= seg.count) {
         // behind the segments: sequences without rows hand their state through, bounds are checked
+        if (!scanner) return;
         for (long long q = sg - seg.count; q < a.num_seqs; q += gridDim.x / nblk - seg.count) {
             long long b, e;
             if (!check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || b != e || a.hT == nullptr || !live) continue;
@@ -65,6 +78,116 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(SsmArgs a, Segments 
 
     const long long t0 = sg * seg.len;
     const long long t1 = t0 + seg.len < a.M ? t0 + seg.len : a.M;
+    SeqRange r{0, 0, 0, false};
+
+    if (!scanner) {
+        // ---- staging: this thread's row of the tile and its eight channels
+        const int srow = tid / VPR, sc0 = (tid % VPR) * 8;
+        const bool stager = tid < TT * VPR;
+        const int scn = stager ? max(0, min(8, cb.n - sc0)) : 0;
+        const int sd = cb.d0 + sc0;
+        const T* xp = static_cast<const T*>(a.x) + sd;
+        const T* dp = static_cast<const T*>(a.delta) + sd;
+        const T* zp = static_cast<const T*>(a.z) + sd;
+        const T* Bp = static_cast<const T*>(a.Bm) + (long long)cb.g * a.N;
+        const T* Cp = static_cast<const T*>(a.Cm) + (long long)cb.g * a.N;
+        float bias[8], dsk[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            bias[i] = i < scn && a.delta_bias ? a.delta_bias[sd + i] : 0.f;
+            dsk[i] = i < scn && a.Dskip ? a.Dskip[sd + i] : 0.f;
+        }
+        Pack<T, 8> nx, nd, nz;
+        Pack<T, 1> nB[kAhead ? BPT : 1], nC[kAhead ? BPT : 1];   // as loaded: converting would wait for the load
+        auto bc = [&](const T* p, long long stride, long long tile, int e) {   // element e of this thread's share
+            const int k = e * kThreads + tid, row = k / NP, n = k % NP;
+            return row < TT && tile + row < t1 && n < a.N ? load_pack<1>(p + (tile + row) * stride + n) : zero_pack<T, 1>();
+        };
+        auto fetch = [&](long long tile) {
+            const long long t = tile + srow;
+            const int n = t < t1 ? scn : 0;
+            nx = load8<T, ALIGNED>(xp + t * a.xs, n);
+            nd = load8<T, ALIGNED>(dp + t * a.ds, n);
+            if (!SUMMARY) nz = a.z ? load8<T, ALIGNED>(zp + t * a.zs, n) : zero_pack<T, 8>();
+            if constexpr (kAhead) {
+#pragma unroll
+                for (int e = 0; e < BPT; ++e) {
+                    nB[e] = bc(Bp, a.bs, tile, e);
+                    if (!SUMMARY) nC[e] = bc(Cp, a.cs, tile, e);
+                }
+            }
+        };
+        auto one = [](const Pack<T, 1>& p) {
+            float f;
+            unpack<T, 1>(p, &f);
+            return f;
+        };
+        auto lay = [&](long long tile, float* buf) {   // the fetched tile into a buffer
+            float *s_dt = buf, *s_u = s_dt + CH * LD, *s_B = s_u + (SUMMARY ? 1 : 2) * CH * LD, *s_C = s_B + TT * NP;
+            if (stager) {
+                float x[8], v[8];
+                unpack<T, 8>(nx, x);
+                unpack<T, 8>(nd, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    v[i] += bias[i];
+                    if (a.softplus) v[i] = softplus(v[i]);
+                    s_dt[(sc0 + i) * LD + srow] = v[i];
+                    s_u[(sc0 + i) * LD + srow] = v[i] * x[i];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < BPT; ++e) {
+                if (e * kThreads + tid >= TT * NP) continue;
+                if constexpr (kAhead) {
+                    s_B[e * kThreads + tid] = one(nB[e]);
+                    if (!SUMMARY) s_C[e * kThreads + tid] = one(nC[e]);
+                } else {
+                    s_B[e * kThreads + tid] = one(bc(Bp, a.bs, tile, e));
+                    if (!SUMMARY) s_C[e * kThreads + tid] = one(bc(Cp, a.cs, tile, e));
+                }
+            }
+        };
+        auto emit = [&](long long tile, const float* buf, const Pack<T, 8>& cx, const Pack<T, 8>& cz) {
+            if constexpr (!SUMMARY) {
+                const float* s_y = buf + 2 * CH * LD;
+                if (!r.ok || tile >= r.e) r = find_seq(a.cu, a.num_seqs, a.M, a.T, tile);
+                if (!stager || tile + srow >= t1) return;
+                if (r.ok && tile + srow < r.e ? false : !find_seq(a.cu, a.num_seqs, a.M, a.T, tile + srow).ok) return;
+                float x[8], z[8], y[8];
+                unpack<T, 8>(cx, x);
+                unpack<T, 8>(cz, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[i] = fmaf(dsk[i], x[i], s_y[(sc0 + i) * LD + srow]);
+                    if (a.z) y[i] *= z[i] * sigmoid<sizeof(T) == 2>(z[i]);
+                }
+                store8<T, ALIGNED>(static_cast<T*>(a.out) + (tile + srow) * a.D + sd, y, scn);
+            }
+        };
+        Pack<T, 8> cx = zero_pack<T, 8>(), cz = zero_pack<T, 8>();
+        int b = 0;
+        fetch(t0);
+        for (long long tile = t0; tile < t1; tile += TT, b ^= 1) {
+            lay(tile, sm + b * kBuf);   // the buffer's last scan ended before the last turn's emit
+            bar_arrive<kFull>(b);
+            const Pack<T, 8> px = cx, pz = cz;
+            cx = nx;
+            cz = nz;
+            if (tile + TT < t1) fetch(tile + TT);
+            if (tile > t0) {
+                bar_sync<kDone>(b ^ 1);
+                emit(tile - TT, sm + (b ^ 1) * kBuf, px, pz);
+            }
+        }
+        if (t1 > t0) {
+            bar_sync<kDone>(b ^ 1);
+            emit(t0 + (t1 - t0 - 1) / TT * TT, sm + (b ^ 1) * kBuf, cx, cz);
+        }
+        return;
+    }
+
+    // ---- scan
     float A2[NS], h[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
@@ -75,45 +198,6 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(SsmArgs a, Segments 
             h[i] = hseg[(sg * a.D + d) * a.N + n];   // used unless a sequence starts at t0
     }
     float dtsum = 0.f;
-
-    // staging: this thread's row of the tile and its eight channels
-    const int srow = tid / VPR, sc0 = (tid % VPR) * 8;
-    const bool stager = tid < TT * VPR;
-    const int scn = stager ? max(0, min(8, cb.n - sc0)) : 0;
-    const int sd = cb.d0 + sc0;
-    const T* xp = static_cast<const T*>(a.x) + sd;
-    const T* dp = static_cast<const T*>(a.delta) + sd;
-    const T* zp = static_cast<const T*>(a.z) + sd;
-    const T* Bp = static_cast<const T*>(a.Bm) + (long long)cb.g * a.N;
-    const T* Cp = static_cast<const T*>(a.Cm) + (long long)cb.g * a.N;
-    float bias[8], dsk[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        bias[i] = i < scn && a.delta_bias ? a.delta_bias[sd + i] : 0.f;
-        dsk[i] = i < scn && a.Dskip ? a.Dskip[sd + i] : 0.f;
-    }
-    Pack<T, 8> nx, nd, nz;
-    float nB[kAhead ? BPT : 1], nC[kAhead ? BPT : 1];
-    auto bc = [&](const T* p, long long stride, long long tile, int e) {   // element e of this thread's share
-        const int k = e * kThreads + tid, row = k / NP, n = k % NP;
-        return row < TT && tile + row < t1 && n < a.N ? to_f32<T>(p[(tile + row) * stride + n]) : 0.f;
-    };
-    auto fetch = [&](long long tile) {
-        const long long t = tile + srow;
-        const int n = t < t1 ? scn : 0;
-        nx = load8<T, ALIGNED>(xp + t * a.xs, n);
-        nd = load8<T, ALIGNED>(dp + t * a.ds, n);
-        if (!SUMMARY) nz = a.z ? load8<T, ALIGNED>(zp + t * a.zs, n) : zero_pack<T, 8>();
-        if constexpr (kAhead) {
-#pragma unroll
-            for (int e = 0; e < BPT; ++e) {
-                nB[e] = bc(Bp, a.bs, tile, e);
-                if (!SUMMARY) nC[e] = bc(Cp, a.cs, tile, e);
-            }
-        }
-    };
-
-    SeqRange r{0, 0, 0, false};
     auto enter = [&](long long t) {   // row t is the first one, or the first behind r
         r = find_seq(a.cu, a.num_seqs, a.M, a.T, t);
         if (r.ok && r.b == t) {
@@ -133,58 +217,44 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(SsmArgs a, Segments 
             }
         }
     };
-    auto row_step = [&](float dt, float u, int i) {   // one row of the tile; the lane's share of y
-        float y = 0.f;
+    int b = 0;
+    for (long long tile = t0; tile < t1; tile += TT, b ^= 1) {
+        float* buf = sm + b * kBuf;
+        const float *s_dt = buf, *s_u = s_dt + CH * LD, *s_B = s_u + (SUMMARY ? 1 : 2) * CH * LD, *s_C = s_B + TT * NP;
+        float* s_y = buf + 2 * CH * LD;
+        auto row_step = [&](float dt, float u, int i) {   // one row of the tile; the lane's share of y
+            F2 acc{0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            h[j] = fmaf(ex2(dt * A2[j]), h[j], u * s_B[i * NP + s * NS + j]);
-            if (!SUMMARY) y = fmaf(h[j], s_C[i * NP + s * NS + j], y);
-        }
-        if (SUMMARY) dtsum += dt;
-        return y;
-    };
-
-    fetch(t0);
-    for (long long tile = t0; tile < t1; tile += TT) {
-        const Pack<T, 8> cx = nx, cz = nz;
-        if (stager) {
-            float x[8], v[8];
-            unpack<T, 8>(nx, x);
-            unpack<T, 8>(nd, v);
+            for (int j = 0; j < NS; j += 4) {
+                const float4 b4 = *reinterpret_cast<const float4*>(&s_B[i * NP + s * NS + j]);
+                float4 c4 = b4;
+                if (!SUMMARY) c4 = *reinterpret_cast<const float4*>(&s_C[i * NP + s * NS + j]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] += bias[i];
-                if (a.softplus) v[i] = softplus(v[i]);
-                s_dt[(sc0 + i) * LD + srow] = v[i];
-                s_u[(sc0 + i) * LD + srow] = v[i] * x[i];
+                for (int m = 0; m < 2; ++m) {
+                    const F2 e = ex2(mul2(both(dt), F2{A2[j + 2 * m], A2[j + 2 * m + 1]}));
+                    const F2 ub = mul2(both(u), m ? F2{b4.z, b4.w} : F2{b4.x, b4.y});
+                    const F2 hn = fma2(e, F2{h[j + 2 * m], h[j + 2 * m + 1]}, ub);
+                    h[j + 2 * m] = hn.x;
+                    h[j + 2 * m + 1] = hn.y;
+                    if (!SUMMARY) acc = fma2(hn, m ? F2{c4.z, c4.w} : F2{c4.x, c4.y}, acc);
+                }
             }
-        }
-#pragma unroll
-        for (int e = 0; e < BPT; ++e) {
-            if (e * kThreads + tid >= TT * NP) continue;
-            if constexpr (kAhead) {
-                s_B[e * kThreads + tid] = nB[e];
-                if (!SUMMARY) s_C[e * kThreads + tid] = nC[e];
-            } else {
-                s_B[e * kThreads + tid] = bc(Bp, a.bs, tile, e);
-                if (!SUMMARY) s_C[e * kThreads + tid] = bc(Cp, a.cs, tile, e);
-            }
-        }
-        __syncthreads();
-        if (tile + TT < t1) fetch(tile + TT);
+            if (SUMMARY) dtsum += dt;
+            return acc.x + acc.y;
+        };
+        bar_sync<kFull>(b);
         const int rows = (int)(t1 - tile < TT ? t1 - tile : TT);
         if (!r.ok || tile >= r.e) enter(tile);
-        const bool whole = rows == TT && r.ok && tile + TT <= r.e;   // the tile lies in one sequence
-        if (whole) {
+        if (rows == TT && r.ok && tile + TT <= r.e) {   // the tile lies in one sequence
 #pragma unroll 2
             for (int i = 0; i < TT; i += 4) {
                 const float4 d4 = *reinterpret_cast<const float4*>(&s_dt[ch * LD + i]);
                 const float4 u4 = *reinterpret_cast<const float4*>(&s_u[ch * LD + i]);
-                const float y0 = row_step(d4.x, u4.x, i);
-                const float y1 = row_step(d4.y, u4.y, i + 1);
-                const float y2 = row_step(d4.z, u4.z, i + 2);
-                const float y3 = row_step(d4.w, u4.w, i + 3);
-                if constexpr (!SUMMARY) lane_sum4<S>(y0, y1, y2, y3, s, &s_y[ch * LD + i]);
+                const float dts[4] = {d4.x, d4.y, d4.z, d4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
+                float y[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) y[k] = row_step(dts[k], us[k], i + k);
+                if constexpr (!SUMMARY) lane_sum4<S>(y[0], y[1], y[2], y[3], s, &s_y[ch * LD + i]);
             }
             if (tile + TT == r.e) finish();
         } else {
@@ -200,20 +270,7 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(SsmArgs a, Segments 
                 if (tile + i + 1 == r.e) finish();
             }
         }
-        __syncthreads();
-        if (!SUMMARY && stager && tile + srow < t1) {
-            if (whole || a.cu == nullptr || find_seq(a.cu, a.num_seqs, a.M, a.T, tile + srow).ok) {
-                float x[8], z[8], y[8];
-                unpack<T, 8>(cx, x);
-                unpack<T, 8>(cz, z);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = fmaf(dsk[i], x[i], s_y[(sc0 + i) * LD + srow]);
-                    if (a.z) y[i] *= z[i] * sigmoid<sizeof(T) == 2>(z[i]);
-                }
-                store8<T, ALIGNED>(static_cast<T*>(a.out) + (tile + srow) * a.D + sd, y, scn);
-            }
-        }
+        bar_arrive<kDone>(b);
     }
     if (SUMMARY && live) {
 #pragma unroll
@@ -223,6 +280,11 @@ __global__ void __launch_bounds__(kThreads) ssm_scan_kernel(SsmArgs a, Segments 
         }
         if (s == 0) dtseg[sg * a.D + d] = dtsum;
     }
+}
+template <int S, int NS, bool SUMMARY>
+constexpr int scan_smem() {
+    constexpr int CH = kThreads / S, TT = tile_rows<S>(), LD = TT + 4, NP = S * NS;
+    return 2 * (int)sizeof(float) * ((SUMMARY ? 2 : 3) * CH * LD + (SUMMARY ? 1 : 2) * TT * NP);
 }
 
 // hseg[k] (the state that segment k alone ends with) -> the state that enters segment k.
@@ -358,18 +420,21 @@ cudaError_t fwd_go(const SsmArgs& a, const Segments& p, cudaStream_t s) {
     const int nblk = (int)blocks;
     float* hseg = reinterpret_cast<float*>(a.ws);
     float* dtseg = hseg + p.count * a.D * a.N;
+    cudaError_t e;
     if (!p.whole) {
-        ssm_scan_kernel<T, S, NS, ALIGNED, true>
-            <<<(unsigned)(blocks * p.count), kThreads, 0, s>>>(a, p, nblk, hseg, dtseg);
-        cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        auto k = ssm_scan_kernel<T, S, NS, ALIGNED, true>;
+        constexpr int sm1 = scan_smem<S, NS, true>();
+        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm1)) != cudaSuccess) return e;
+        k<<<(unsigned)(blocks * p.count), 2 * kThreads, sm1, s>>>(a, p, nblk, hseg, dtseg);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         const long long dn = (long long)a.D * a.N;
         ssm_join_kernel<<<(unsigned)((dn + 127) / 128), 128, (size_t)p.count, s>>>(a, p, hseg, dtseg);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    ssm_scan_kernel<T, S, NS, ALIGNED, false>
-        <<<(unsigned)(blocks * (p.count + extra)), kThreads, 0, s>>>(a, p, nblk, hseg, dtseg);
+    auto k = ssm_scan_kernel<T, S, NS, ALIGNED, false>;
+    constexpr int sm2 = scan_smem<S, NS, false>();
+    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm2)) != cudaSuccess) return e;
+    k<<<(unsigned)(blocks * (p.count + extra)), 2 * kThreads, sm2, s>>>(a, p, nblk, hseg, dtseg);
     return cudaGetLastError();
 }
 

@@ -9,22 +9,30 @@
 //     ddt    = sum_n q[n] A[n] + p x,   dx = p dt + Dskip dy
 //     dh[n]  <- w[n]                                  (dh0 in front of the first row)
 //
-// The rows are cut into segments of L, aligned to the row index.
+// The rows are cut into segments, aligned to the row index.
 //   1. summary: every segment alone, scanned once from zero, gives its last state, the
 //      gradient that its rows send to the state in front of it (sum_t (prod a) C dy, the
-//      running product taken along, so no second exponential), and the sum of dt.
+//      running product taken along, so no second exponential), the sum of dt, and both
+//      states and sums in front of every 8 rows (checkpoints).
 //   2. join: along the segments, forward for the incoming states, backward for the
 //      incoming state gradients (the decay over a segment is e^{A sum dt}).
-//   3. gradients, all segments in parallel: a forward scan keeps the state in front of
-//      every SUB rows; then, from the last SUB rows back, their states and decays are
-//      computed again into registers and walked in reverse.
+//   3. gradients, all segments in parallel, each from its last 8 rows back: the checkpoint
+//      plus the decayed incoming state, then the 8 rows' states and decays into registers,
+//      then the 8 rows in reverse.
 //   4. sums: of dB and dC over the channel blocks, of dA, dDskip and the bias over segments.
-// Three sets of exponentials and about 21 fp32 operations per row, channel and state: the
-// fp32 and special-function units bound it, not the bytes.
+// Two sets of exponentials (and one in 8 rows for the checkpoints) and about 18 fp32
+// operations per row, channel and state: the special-function, fp32 and shared-memory
+// pipes are all near their limits at once; the bytes take a fifth of the time.
 //
-// Lanes as in the forward: S lanes of a channel, NS states each, 128 / S channels of a CTA.
-// dB and dC sum over a warp's channels by halving exchanges: of 2 NS values, every lane of
-// a channel set ends with its own few sums.
+// Lanes: S lanes of a channel pair, four states each (as two register pairs for the packed
+// fp32 instructions); a thread takes two channels, so that B and C are read from shared
+// memory once for both and dB, dC are added over both before any exchange.  A CTA of 128
+// threads holds 256 / S channels.  Sums over lanes are taken by halving exchanges: a lane
+// keeps one half of its values and sends the other.  Where the halves are register pairs or
+// channels, lanes on the upper side hold them in swapped order, so that every lane keeps the
+// same registers and nothing is selected.
+#include <type_traits>
+
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -33,64 +41,71 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
+constexpr int kSub = 8;        // rows between checkpoints
 
 template <int S>
-constexpr int seg_rows() { return S >= 4 ? 64 : 32; }
+constexpr int channels() { return 2 * kThreads / S; }
+template <int S>
+constexpr int tile_rows() { return S >= 4 ? 32 : 8 * S; }
 
-// First / last rows of sequences and rows of any sequence, one bit per row of the segment.
+// First / last rows of sequences and rows of any sequence, one bit per row of the tile.
 struct Events {
-    uint32_t first[2], last[2], in[2];
+    uint32_t first, last, in;
 };
-__device__ __forceinline__ bool bit(const uint32_t* m, int i) { return m[i >> 5] >> (i & 31) & 1; }
-
-template <int L>
-__device__ __forceinline__ void find_events(const SsmArgs& a, long long t0, Events* ev) {
-    const int i = threadIdx.x;
-    if (i < L) {
-        SeqRange r{0, 0, 0, false};
-        if (t0 + i < a.M) r = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + i);
-        const uint32_t f = __ballot_sync(0xffffffffu, r.ok && r.b == t0 + i);
-        const uint32_t l = __ballot_sync(0xffffffffu, r.ok && r.e == t0 + i + 1);
-        const uint32_t in = __ballot_sync(0xffffffffu, r.ok);
-        if ((i & 31) == 0) {
-            ev->first[i >> 5] = f;
-            ev->last[i >> 5] = l;
-            ev->in[i >> 5] = in;
-        }
-    }
+__device__ __forceinline__ Events find_events(const SsmArgs& a, long long t0, int rows) {   // whole warps
+    const int i = threadIdx.x & 31;
+    SeqRange r{0, 0, 0, false};
+    if (i < rows && t0 + i < a.M) r = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + i);
+    Events e;
+    e.first = __ballot_sync(0xffffffffu, r.ok && r.b == t0 + i);
+    e.last = __ballot_sync(0xffffffffu, r.ok && r.e == t0 + i + 1);
+    e.in = __ballot_sync(0xffffffffu, r.ok);
+    return e;
 }
 
-// dt, x (or dt x) and dy of the segment into shared memory [channel][row]; zeros in rows
+// A pair of B or C in shared memory (as stored, two bf16 or two fp32).
+__device__ __forceinline__ F2 lds_pair(const float* p) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    return F2{v.x, v.y};
+}
+__device__ __forceinline__ F2 lds_pair(const __nv_bfloat16* p) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    return F2{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+}
+__device__ __forceinline__ F2 shfl2(F2 v, int m) {
+    return F2{__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m)};
+}
+
+// dt, x (or dt x) and dy of the tile into shared memory [channel][row]; zeros in rows
 // that no sequence covers, which then neither decay nor add anything.
-template <typename T, int CH, int L, int LD, bool ALIGNED, bool TIMES>
-__device__ __forceinline__ void stage(const SsmArgs& a, const ChannelBlock& cb, long long t0, const Events& ev, float* s_dt,
+template <typename T, int CH, int TT, int LD, bool ALIGNED, bool TIMES>
+__device__ __forceinline__ void stage(const SsmArgs& a, const ChannelBlock& cb, long long t0, uint32_t in, float* s_dt,
                                       float* s_x, float* s_dy) {
-    constexpr int VPR = CH / 8, RPP = kThreads / VPR;   // rows per pass
-    const int c0 = (threadIdx.x % VPR) * 8;
-    const int cn = max(0, min(8, cb.n - c0)), d = cb.d0 + c0;
-    float bias[8];
+    constexpr int VPR = CH / 8;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) bias[i] = i < cn && a.delta_bias ? a.delta_bias[d + i] : 0.f;
-#pragma unroll
-    for (int row0 = 0; row0 < L; row0 += RPP) {
-        const int row = row0 + threadIdx.x / VPR;
-        if (row >= L) break;
+    for (int it = 0; it < (TT * VPR + kThreads - 1) / kThreads; ++it) {
+        const int slot = it * kThreads + threadIdx.x, row = slot / VPR, c0 = (slot % VPR) * 8;
+        if (row >= TT) break;
+        const int cn = max(0, min(8, cb.n - c0)), d = cb.d0 + c0;
         const long long t = t0 + row;
-        const bool in = bit(ev.in, row);
-        const int n = in ? cn : 0;
+        const int n = in >> row & 1 ? cn : 0;
+        const Pack<T, 8> px = load8<T, ALIGNED>(static_cast<const T*>(a.x) + t * a.xs + d, n);
+        const Pack<T, 8> pv = load8<T, ALIGNED>(static_cast<const T*>(a.delta) + t * a.ds + d, n);
+        const Pack<T, 8> pg = load8<T, ALIGNED>(static_cast<const T*>(a.d_out) + t * a.D + d, n);
+        const Pack<T, 8> pz = a.z ? load8<T, ALIGNED>(static_cast<const T*>(a.z) + t * a.zs + d, n) : zero_pack<T, 8>();
         float x[8], v[8], g[8];
-        unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.x) + t * a.xs + d, n), x);
-        unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.delta) + t * a.ds + d, n), v);
-        unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.d_out) + t * a.D + d, n), g);
+        unpack<T, 8>(px, x);
+        unpack<T, 8>(pv, v);
+        unpack<T, 8>(pg, g);
         if (a.z != nullptr) {
             float z[8];
-            unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.z) + t * a.zs + d, n), z);
+            unpack<T, 8>(pz, z);
 #pragma unroll
             for (int i = 0; i < 8; ++i) g[i] *= z[i] * sigmoid<sizeof(T) == 2>(z[i]);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[i] += bias[i];
+            if (a.delta_bias && i < n) v[i] += __ldg(a.delta_bias + d + i);
             if (a.softplus) v[i] = softplus(v[i]);
             if (i >= n) v[i] = 0.f;
             s_dt[(c0 + i) * LD + row] = v[i];
@@ -100,16 +115,16 @@ __device__ __forceinline__ void stage(const SsmArgs& a, const ChannelBlock& cb, 
     }
 }
 
-template <typename T, int L, int NP>
-__device__ __forceinline__ void stage_bc(const SsmArgs& a, int g, long long t0, const Events& ev, float* s_B, float* s_C) {
+template <typename T, int TT, int NP>
+__device__ __forceinline__ void stage_bc(const SsmArgs& a, int g, long long t0, uint32_t in, T* s_B, T* s_C) {
     const T* Bp = static_cast<const T*>(a.Bm) + (long long)g * a.N;
     const T* Cp = static_cast<const T*>(a.Cm) + (long long)g * a.N;
-#pragma unroll 8
-    for (int k = threadIdx.x; k < L * NP; k += kThreads) {
+#pragma unroll 4
+    for (int k = threadIdx.x; k < TT * NP; k += kThreads) {
         const int row = k / NP, n = k % NP;
-        const bool on = n < a.N && bit(ev.in, row);
-        s_B[k] = on ? to_f32<T>(Bp[(t0 + row) * a.bs + n]) : 0.f;
-        s_C[k] = on ? to_f32<T>(Cp[(t0 + row) * a.cs + n]) : 0.f;
+        const bool on = n < a.N && (in >> row & 1);
+        s_B[k] = on ? Bp[(t0 + row) * a.bs + n] : from_f32<T>(0.f);
+        s_C[k] = on ? Cp[(t0 + row) * a.cs + n] : from_f32<T>(0.f);
     }
 }
 
@@ -118,361 +133,485 @@ constexpr uint8_t kStarts = 1;      // holds a sequence's first row (its last st
 constexpr uint8_t kEnds = 2;        // the sequence of its first row ends in it
 constexpr uint8_t kFirst = 4;       // its first row is a sequence's first row
 
-template <typename T, int S, int NS, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) ssm_bwd_summary_kernel(SsmArgs a, long long K, int nblk, float* hseg,
-                                                                  float* rseg, float* dtseg, uint8_t* flags) {
-    constexpr int CH = kThreads / S, L = seg_rows<S>(), LD = L + 4, NP = S * NS;
+// This thread's channels and states: channel slot k (of two), register pair m (of two).
+template <int S>
+struct Place {
+    static constexpr int CH = channels<S>(), NP = 4 * S;
+    int lane, warp, s, csw, sw, d[2];
+    bool live[2];
+    int ch[2];
+    __device__ __forceinline__ Place(const ChannelBlock& cb) {
+        const int tid = threadIdx.x;
+        lane = tid & 31;
+        warp = tid >> 5;
+        s = tid % S;
+        csw = S >= 2 ? tid & 1 : 0;           // lanes on the upper side of the first channel exchange
+        sw = S <= 16 ? tid >> 4 & 1 : 0;      // .. and of the first state exchange
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            ch[k] = tid / S + (k ^ csw) * (CH / 2);
+            live[k] = ch[k] < cb.n;
+            d[k] = cb.d0 + (live[k] ? ch[k] : 0);
+        }
+    }
+    __device__ __forceinline__ int n(int m) const { return s * 4 + 2 * (m ^ sw); }   // first state of pair m
+    // a pair of a caller's [.., D, N] array, at row q
+    __device__ __forceinline__ F2 get(const float* p, long long q, const SsmArgs& a, int k, int m) const {
+        F2 v{0.f, 0.f};
+        if (p == nullptr || !live[k]) return v;
+        const float* at = p + (q * a.D + d[k]) * a.N + n(m);
+        if (n(m) < a.N) v.x = at[0];
+        if (n(m) + 1 < a.N) v.y = at[1];
+        return v;
+    }
+    __device__ __forceinline__ void put(float* p, long long q, const SsmArgs& a, int k, int m, F2 v) const {
+        if (p == nullptr || !live[k]) return;
+        float* at = p + (q * a.D + d[k]) * a.N + n(m);
+        if (n(m) < a.N) at[0] = v.x;
+        if (n(m) + 1 < a.N) at[1] = v.y;
+    }
+    // the same in a workspace array [.., D, NP]
+    __device__ __forceinline__ F2 load(const float* p, long long q, int D, int k, int m) const {
+        if (!live[k]) return F2{0.f, 0.f};
+        const float2 v = *reinterpret_cast<const float2*>(p + (q * D + d[k]) * NP + n(m));
+        return F2{v.x, v.y};
+    }
+    __device__ __forceinline__ void store(float* p, long long q, int D, int k, int m, F2 v) const {
+        if (live[k]) *reinterpret_cast<float2*>(p + (q * D + d[k]) * NP + n(m)) = make_float2(v.x, v.y);
+    }
+};
+
+template <typename T, int S>
+constexpr size_t summary_smem() {
+    return sizeof(float) * 3 * channels<S>() * (tile_rows<S>() + 4) + sizeof(T) * 2 * tile_rows<S>() * 4 * S;
+}
+
+template <typename T, int S, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a, Segments seg, int nblk, float* hseg,
+                                                                     float* rseg, float* dtseg, float* hck, float* dtck,
+                                                                     uint8_t* flags) {
+    constexpr int CH = channels<S>(), TT = tile_rows<S>(), LD = TT + 4, NP = 4 * S;
     extern __shared__ __align__(16) float sm[];
-    float *s_dt = sm, *s_u = s_dt + CH * LD, *s_dy = s_u + CH * LD, *s_B = s_dy + CH * LD, *s_C = s_B + L * NP;
-    __shared__ Events ev;
+    float *s_dt = sm, *s_u = s_dt + CH * LD, *s_dy = s_u + CH * LD;
+    T *s_B = reinterpret_cast<T*>(s_dy + CH * LD), *s_C = s_B + TT * NP;
     const long long sg = blockIdx.x / nblk;
     const ChannelBlock cb = channel_block<CH>(blockIdx.x % nblk, a.D, a.G);
-    const int tid = threadIdx.x, ch = tid / S, s = tid % S;
-    const bool live = ch < cb.n;
-    const int d = cb.d0 + (live ? ch : 0);
-    if (sg >= K) {   // sequences without rows hand their state's gradient through
-        for (long long q = sg - K; q < a.num_seqs; q += gridDim.x / nblk - K) {
+    const Place<S> at(cb);
+    if (sg >= seg.count) {   // sequences without rows hand their state's gradient through
+        for (long long q = sg - seg.count; q < a.num_seqs; q += gridDim.x / nblk - seg.count) {
             long long b, e;
-            if (!check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || b != e || a.dh0 == nullptr || !live) continue;
-            const long long at = (q * a.D + d) * a.N;
-            for (int n = s * NS; n < s * NS + NS && n < a.N; ++n) a.dh0[at + n] = a.d_hT ? a.d_hT[at + n] : 0.f;
+            if (!check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || b != e) continue;
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) at.put(a.dh0, q, a, k, m, at.get(a.d_hT, q, a, k, m));
         }
         return;
     }
-    const long long t0 = sg * L;
-    find_events<L>(a, t0, &ev);
-    __syncthreads();
-    stage<T, CH, L, LD, ALIGNED, true>(a, cb, t0, ev, s_dt, s_u, s_dy);
-    stage_bc<T, L, NP>(a, cb.g, t0, ev, s_B, s_C);
-    float A2[NS], h[NS], p[NS], g[NS];
+    const long long t0 = sg * seg.len, t1 = t0 + seg.len < a.M ? t0 + seg.len : a.M;
+    F2 A2[2][2], h[2][2], p[2][2], g[2][2];
+    float dtsum[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        const int n = s * NS + j;
-        A2[j] = live && n < a.N ? a.A[(long long)d * a.N + n] * kLog2e : 0.f;
-        h[j] = g[j] = 0.f;
-        p[j] = 1.f;
-    }
-    float dtsum = 0.f;
-    auto state_of = [&](const float* from, long long t, int j) {   // a state of the sequence of row t
-        const int n = s * NS + j;
-        if (from == nullptr || !live || n >= a.N) return 0.f;
-        const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, t);
-        return from[((long long)r.q * a.D + d) * a.N + n];
-    };
-    __syncthreads();
-#pragma unroll 2
-    for (int i = 0; i < L; i += 4) {
-        const float4 d4 = *reinterpret_cast<const float4*>(&s_dt[ch * LD + i]);
-        const float4 u4 = *reinterpret_cast<const float4*>(&s_u[ch * LD + i]);
-        const float4 g4 = *reinterpret_cast<const float4*>(&s_dy[ch * LD + i]);
-        const float dts[4] = {d4.x, d4.y, d4.z, d4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w}, gs[4] = {g4.x, g4.y, g4.z, g4.w};
-        const uint32_t mf = ev.first[i >> 5] >> (i & 31), ml = ev.last[i >> 5] >> (i & 31);
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (mf >> k & 1) {
+        for (int m = 0; m < 2; ++m) {
+            A2[k][m] = mul2(at.get(a.A, 0, a, k, m), both(kLog2e));
+            h[k][m] = g[k][m] = F2{0.f, 0.f};
+            p[k][m] = F2{1.f, 1.f};
+        }
+    uint8_t f = 0;
+    for (long long tile = t0; tile < t1; tile += TT) {
+        const Events ev = find_events(a, tile, TT);
+        if (tile == t0 && ((ev.first & 1) || !(ev.in & 1))) f |= kFirst;
+        if (tile == t0 && !(ev.in & 1)) f |= kEnds;
+        if (ev.first) f |= kStarts;
+        if (ev.last) f |= kEnds;
+        if (tile != t0) __syncthreads();
+        stage<T, CH, TT, LD, ALIGNED, true>(a, cb, tile, ev.in, s_dt, s_u, s_dy);
+        stage_bc<T, TT, NP>(a, cb.g, tile, ev.in, s_B, s_C);
+        __syncthreads();
+#pragma unroll 1
+        for (int i0 = 0; i0 < TT; i0 += kSub) {
+            if (tile + i0 >= t1) break;
+            const long long r8 = (tile + i0) / kSub;
 #pragma unroll
-                for (int j = 0; j < NS; ++j) {
-                    h[j] = state_of(a.h0, t0 + i + k, j);
-                    if (i + k > 0) p[j] = 0.f;   // rows behind the first sequence's end
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int m = 0; m < 2; ++m) at.store(hck, r8, a.D, k, m, h[k][m]);
+                if (at.s == 0 && at.live[k]) dtck[r8 * a.D + at.d[k]] = dtsum[k];
+            }
+            auto rows = [&](auto evc) {   // eight rows, with or without sequences that begin or end there
+                constexpr bool EV = decltype(evc)::value;
+#pragma unroll
+                for (int i = i0; i < i0 + kSub; i += 4) {
+                    float4 d4[2], u4[2], g4[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[at.ch[k] * LD + i]);
+                        u4[k] = *reinterpret_cast<const float4*>(&s_u[at.ch[k] * LD + i]);
+                        g4[k] = *reinterpret_cast<const float4*>(&s_dy[at.ch[k] * LD + i]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (EV && (ev.first >> (i + j) & 1)) {
+                            const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, tile + i + j);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) {
+                                    h[k][m] = at.get(a.h0, r.q, a, k, m);
+                                    if (tile + i + j > t0) p[k][m] = F2{0.f, 0.f};   // behind the first sequence's end
+                                }
+                        }
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const F2 B = lds_pair(s_B + (i + j) * NP + at.n(m)), C = lds_pair(s_C + (i + j) * NP + at.n(m));
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float dt = j == 0 ? d4[k].x : j == 1 ? d4[k].y : j == 2 ? d4[k].z : d4[k].w;
+                                const float u = j == 0 ? u4[k].x : j == 1 ? u4[k].y : j == 2 ? u4[k].z : u4[k].w;
+                                const float dy = j == 0 ? g4[k].x : j == 1 ? g4[k].y : j == 2 ? g4[k].z : g4[k].w;
+                                const F2 e = ex2(mul2(both(dt), A2[k][m]));
+                                h[k][m] = fma2(e, h[k][m], mul2(both(u), B));
+                                p[k][m] = mul2(p[k][m], e);
+                                g[k][m] = fma2(p[k][m], mul2(both(dy), C), g[k][m]);
+                                if (m == 0) dtsum[k] += dt;
+                            }
+                        }
+                        if (EV && (ev.last >> (i + j) & 1)) {
+                            const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, tile + i + j);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                                for (int m = 0; m < 2; ++m) {
+                                    g[k][m] = fma2(p[k][m], at.get(a.d_hT, r.q, a, k, m), g[k][m]);
+                                    p[k][m] = F2{0.f, 0.f};
+                                }
+                        }
+                    }
                 }
-            }
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const float e = ex2(dts[k] * A2[j]);
-                h[j] = fmaf(e, h[j], us[k] * s_B[(i + k) * NP + s * NS + j]);
-                p[j] *= e;
-                g[j] = fmaf(p[j], gs[k] * s_C[(i + k) * NP + s * NS + j], g[j]);
-            }
-            dtsum += dts[k];
-            if (ml >> k & 1) {
-#pragma unroll
-                for (int j = 0; j < NS; ++j) {
-                    if (a.d_hT != nullptr) g[j] = fmaf(p[j], state_of(a.d_hT, t0 + i + k, j), g[j]);
-                    p[j] = 0.f;
-                }
-            }
+            };
+            if ((ev.first | ev.last) >> i0 & 0xff) rows(std::true_type{});
+            else rows(std::false_type{});
         }
     }
-    if (live) {
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-            const int n = s * NS + j;
-            if (n < a.N) {
-                hseg[(sg * a.D + d) * a.N + n] = h[j];
-                rseg[(sg * a.D + d) * a.N + n] = g[j];
-            }
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            at.store(hseg, sg, a.D, k, m, h[k][m]);
+            at.store(rseg, sg, a.D, k, m, g[k][m]);
         }
-        if (s == 0) dtseg[sg * a.D + d] = dtsum;
+        if (at.s == 0 && at.live[k]) dtseg[sg * a.D + at.d[k]] = dtsum[k];
     }
-    if (blockIdx.x % nblk == 0 && tid == 0) {
-        uint8_t f = 0;
-        if (ev.first[0] | (L > 32 ? ev.first[1] : 0u)) f |= kStarts;
-        if (ev.last[0] | (L > 32 ? ev.last[1] : 0u) | !(ev.in[0] & 1)) f |= kEnds;
-        if ((ev.first[0] & 1) || !(ev.in[0] & 1)) f |= kFirst;
-        flags[sg] = f;
-    }
+    if (blockIdx.x % nblk == 0 && threadIdx.x == 0) flags[sg] = f;
 }
 
 // y = 0: hseg[k] (segment k's own last state) -> the state in front of it.
 // y = 1: rseg[k] (what its rows send to the state in front) -> the gradient of its last state.
-__global__ void __launch_bounds__(128) ssm_bwd_join_kernel(SsmArgs a, long long K, float* hseg, float* rseg,
+// A chain along the segments; eight segments' values are loaded ahead of their use.
+__global__ void __launch_bounds__(128) ssm_bwd_join_kernel(SsmArgs a, int NP, long long K, float* hseg, float* rseg,
                                                            const float* dtseg, const uint8_t* flags) {
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, DN = (long long)a.D * a.N;
+    constexpr int U = 8;
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, DN = (long long)a.D * NP;
     if (i >= DN) return;
-    const float A2 = a.A[i] * kLog2e;
-    const long long d = i / a.N;
+    const long long d = i / NP;
+    const int n = (int)(i - d * NP);
+    const float A2 = n < a.N ? a.A[d * a.N + n] * kLog2e : 0.f;
+    const bool fwd = blockIdx.y == 0;
+    float* v = fwd ? hseg : rseg;
     float c = 0.f;
-    if (blockIdx.y == 0) {
-#pragma unroll 8
-        for (long long k = 0; k < K; ++k) {
-            const float own = hseg[k * DN + i], dt = dtseg[k * a.D + d];
-            const uint8_t f = flags[k];
-            hseg[k * DN + i] = c;
-            c = f & kStarts ? own : fmaf(ex2(dt * A2), c, own);
+    for (long long k0 = 0; k0 < K; k0 += U) {
+        float own[U], dec[U];
+        uint8_t f[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long k = fwd ? k0 + u : K - 1 - k0 - u;
+            const bool in = k0 + u < K;
+            own[u] = in ? v[k * DN + i] : 0.f;
+            dec[u] = in ? dtseg[k * a.D + d] : 0.f;
+            f[u] = in ? flags[k] : 0;
         }
-    } else {
-#pragma unroll 8
-        for (long long k = K - 1; k >= 0; --k) {
-            const float own = rseg[k * DN + i], dt = dtseg[k * a.D + d];
-            const uint8_t f = flags[k];
-            rseg[k * DN + i] = c;
-            c = f & kFirst ? 0.f : f & kEnds ? own : fmaf(ex2(dt * A2), c, own);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const long long k = fwd ? k0 + u : K - 1 - k0 - u;
+            if (k0 + u >= K) break;
+            v[k * DN + i] = c;
+            const float through = fmaf(ex2(dec[u] * A2), c, own[u]);
+            if (fwd) c = f[u] & kStarts ? own[u] : through;
+            else c = f[u] & kFirst ? 0.f : f[u] & kEnds ? own[u] : through;
         }
     }
 }
 
-template <int S, int NS, int SUB>
-constexpr size_t grad_smem() {
-    constexpr int CH = kThreads / S, L = seg_rows<S>(), LD = L + 4, NP = S * NS;
-    return sizeof(float) * (6 * CH * LD + 2 * L * NP + (L / SUB) * NS * kThreads + 2 * kWarps * SUB * 2 * NP);
+// The sums over a channel's S lanes of four rows' values v[slot][row], written to
+// to[channel * LD + row]: channels are exchanged first (in swapped order), then rows.
+template <int S, int LD>
+__device__ __forceinline__ void lane_sum42(const Place<S>& at, float (&v)[2][4], float* to) {
+    if constexpr (S == 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<float4*>(to + at.ch[k] * LD) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
+    } else {
+        F2 lo = add2(F2{v[0][0], v[0][1]}, shfl2(F2{v[1][0], v[1][1]}, 1));
+        F2 hi = add2(F2{v[0][2], v[0][3]}, shfl2(F2{v[1][2], v[1][3]}, 1));
+        if constexpr (S == 2) {
+            *reinterpret_cast<float4*>(to + at.ch[0] * LD) = make_float4(lo.x, lo.y, hi.x, hi.y);
+        } else {
+            const bool up = at.s & 2;   // keeps rows 2 and 3
+            F2 keep = up ? hi : lo;
+            keep = add2(keep, shfl2(up ? lo : hi, 2));
+#pragma unroll
+            for (int m = 4; m < S; m <<= 1) keep = add2(keep, shfl2(keep, m));
+            if (at.s < 4) *reinterpret_cast<float2*>(to + at.ch[0] * LD + (up ? 2 : 0)) = make_float2(keep.x, keep.y);
+        }
+    }
 }
 
-template <typename T, int S, int NS, int SUB, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads) ssm_bwd_grad_kernel(SsmArgs a, long long K, int nblk, const float* hseg,
-                                                                const float* rseg, float* part, float* bcpart) {
-    constexpr int CH = kThreads / S, L = seg_rows<S>(), LD = L + 4, NP = S * NS;
-    constexpr int VPR = CH / 8, RPP = kThreads / VPR;
-    constexpr int V = 2 * NS, CL = 32 / S, RV = V / CL > 0 ? V / CL : 1;   // sums per lane of dB, dC
+// The sums over a warp's channels of a row's dB and dC pairs, written to red[2][NP].
+template <int S>
+__device__ __forceinline__ void channel_sum(const Place<S>& at, const F2 (&dB)[2], const F2 (&dC)[2], float* red) {
+    constexpr int NP = 4 * S;
+    const int n0 = at.n(0);
+    if constexpr (S == 32) {
+        *reinterpret_cast<float4*>(red + n0) = make_float4(dB[0].x, dB[0].y, dB[1].x, dB[1].y);
+        *reinterpret_cast<float4*>(red + NP + n0) = make_float4(dC[0].x, dC[0].y, dC[1].x, dC[1].y);
+    } else {
+        const F2 b = add2(dB[0], shfl2(dB[1], 16)), c = add2(dC[0], shfl2(dC[1], 16));
+        if constexpr (S == 16) {
+            *reinterpret_cast<float2*>(red + n0) = make_float2(b.x, b.y);
+            *reinterpret_cast<float2*>(red + NP + n0) = make_float2(c.x, c.y);
+        } else {
+            const bool up = at.lane & 8;   // keeps dC
+            F2 k = up ? c : b;
+            k = add2(k, shfl2(up ? b : c, 8));
+            if constexpr (S == 8) {
+                *reinterpret_cast<float2*>(red + (up ? NP : 0) + n0) = make_float2(k.x, k.y);
+            } else {
+                const bool odd = at.lane & 4;   // keeps the pair's second state
+                float o = odd ? k.y : k.x;
+                o += __shfl_xor_sync(0xffffffffu, odd ? k.x : k.y, 4);
+#pragma unroll
+                for (int m = 2; m >= S; m >>= 1) o += __shfl_xor_sync(0xffffffffu, o, m);
+                if ((at.lane & 3) < S) red[(up ? NP : 0) + n0 + odd] = o;
+            }
+        }
+    }
+}
+
+template <typename T, int S>
+constexpr size_t grad_smem() {
+    return sizeof(float) * (6 * channels<S>() * (tile_rows<S>() + 4) + 2 * kWarps * kSub * 2 * 4 * S) +
+           sizeof(T) * 2 * tile_rows<S>() * 4 * S;
+}
+
+template <typename T, int S, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(SsmArgs a, Segments seg, int nblk, const float* hseg,
+                                                                  const float* rseg, const float* hck, const float* dtck,
+                                                                  float* part, float* bcpart) {
+    constexpr int CH = channels<S>(), TT = tile_rows<S>(), LD = TT + 4, NP = 4 * S, VPR = CH / 8;
     extern __shared__ __align__(16) float sm[];
     float *s_dt = sm, *s_x = s_dt + CH * LD, *s_dy = s_x + CH * LD;
-    float *s_p = s_dy + CH * LD, *s_q = s_p + CH * LD, *s_y = s_q + CH * LD;
-    float *s_B = s_y + CH * LD, *s_C = s_B + L * NP, *s_ck = s_C + L * NP, *s_red = s_ck + (L / SUB) * NS * kThreads;
-    __shared__ Events ev;
+    float *s_p = s_dy + CH * LD, *s_q = s_p + CH * LD, *s_y = s_q + CH * LD, *s_red = s_y + CH * LD;
+    T *s_B = reinterpret_cast<T*>(s_red + 2 * kWarps * kSub * 2 * NP), *s_C = s_B + TT * NP;
     const long long sg = blockIdx.x / nblk;
-    const int blk = blockIdx.x % nblk;
+    const int blk = blockIdx.x % nblk, tid = threadIdx.x;
     const ChannelBlock cb = channel_block<CH>(blk, a.D, a.G);
-    const int tid = threadIdx.x, ch = tid / S, s = tid % S, lane = tid & 31, warp = tid >> 5;
-    const bool live = ch < cb.n;
-    const int d = cb.d0 + (live ? ch : 0);
-    const long long t0 = sg * L;
-    find_events<L>(a, t0, &ev);
-    __syncthreads();
-    stage<T, CH, L, LD, ALIGNED, false>(a, cb, t0, ev, s_dt, s_x, s_dy);
-    stage_bc<T, L, NP>(a, cb.g, t0, ev, s_B, s_C);
+    const Place<S> at(cb);
+    const long long t0 = sg * seg.len, t1 = t0 + seg.len < a.M ? t0 + seg.len : a.M;
+    // rows that the segment's incoming state reaches: those of the sequence it is cut out of
+    const SeqRange r0 = find_seq(a.cu, a.num_seqs, a.M, a.T, t0);
+    const long long reach = r0.ok && r0.b < t0 ? r0.e : t0;
 
-    float A2[NS], h[NS], dh[NS], dA[NS];
+    F2 A2[2][2], dh[2][2], dA[2][2];
 #pragma unroll
-    for (int j = 0; j < NS; ++j) {
-        const int n = s * NS + j;
-        const bool on = live && n < a.N;
-        A2[j] = on ? a.A[(long long)d * a.N + n] * kLog2e : 0.f;
-        h[j] = on ? hseg[(sg * a.D + d) * a.N + n] : 0.f;
-        dh[j] = on ? rseg[(sg * a.D + d) * a.N + n] : 0.f;
-        dA[j] = 0.f;
-    }
-    auto state_of = [&](const float* from, int i, int j) {
-        const int n = s * NS + j;
-        if (from == nullptr || !live || n >= a.N) return 0.f;
-        const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + i);
-        return from[((long long)r.q * a.D + d) * a.N + n];
-    };
-    __syncthreads();
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            A2[k][m] = mul2(at.get(a.A, 0, a, k, m), both(kLog2e));
+            dh[k][m] = at.load(rseg, sg, a.D, k, m);
+            dA[k][m] = F2{0.f, 0.f};
+        }
+    float sD[8] = {}, sb[8] = {};
+    int phase = 0;
 
-    // forward: the state in front of every SUB rows
-#pragma unroll 1
-    for (int sb = 0; sb < L / SUB; ++sb) {
-#pragma unroll
-        for (int j = 0; j < NS; ++j) s_ck[(sb * NS + j) * kThreads + tid] = h[j];
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-            const int r = sb * SUB + i;
-            if (bit(ev.first, r)) {
-#pragma unroll
-                for (int j = 0; j < NS; ++j) h[j] = state_of(a.h0, r, j);
-            }
-            const float dt = s_dt[ch * LD + r], u = dt * s_x[ch * LD + r];
-#pragma unroll
-            for (int j = 0; j < NS; ++j) h[j] = fmaf(ex2(dt * A2[j]), h[j], u * s_B[r * NP + s * NS + j]);
-        }
-    }
-
-    // which of a row's 2 NS sums this lane ends with, and whether it is the one to write them
-    int off = 0;
-    bool writer = true;
-    {
-        int cnt = V;
-#pragma unroll
-        for (int m = 16; m >= S; m >>= 1) {
-            if (cnt > 1) {
-                cnt /= 2;
-                if (lane & m) off += cnt;
-            } else if (lane & m) {
-                writer = false;
-            }
-        }
-    }
-
-    const int rows = (int)(a.M - t0 < L ? a.M - t0 : L);
-#pragma unroll 1
-    for (int sb = L / SUB - 1; sb >= 0; --sb) {
-        float ha[SUB][NS], ea[SUB][NS], hs[NS];
-#pragma unroll
-        for (int j = 0; j < NS; ++j) hs[j] = h[j] = s_ck[(sb * NS + j) * kThreads + tid];
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-            const int r = sb * SUB + i;
-            if (bit(ev.first, r)) {
-#pragma unroll
-                for (int j = 0; j < NS; ++j) h[j] = state_of(a.h0, r, j);
-            }
-            const float dt = s_dt[ch * LD + r], u = dt * s_x[ch * LD + r];
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                ea[i][j] = ex2(dt * A2[j]);
-                h[j] = fmaf(ea[i][j], h[j], u * s_B[r * NP + s * NS + j]);
-                ha[i][j] = h[j];
-            }
-        }
-        float* red = s_red + ((sb & 1) * kWarps + warp) * SUB * 2 * NP;
-        float pv[4], qv[4], yv[4];
-#pragma unroll
-        for (int i = SUB - 1; i >= 0; --i) {
-            const int r = sb * SUB + i;
-            if (bit(ev.last, r)) {
-#pragma unroll
-                for (int j = 0; j < NS; ++j) dh[j] = state_of(a.d_hT, r, j);
-            }
-            const bool first = bit(ev.first, r);
-            const float dt = s_dt[ch * LD + r], u = dt * s_x[ch * LD + r], dy = s_dy[ch * LD + r];
-            float v[V], p = 0.f, q = 0.f, y = 0.f;
-#pragma unroll
-            for (int j = 0; j < NS; ++j) {
-                const float B = s_B[r * NP + s * NS + j], C = s_C[r * NP + s * NS + j];
-                float hp = i > 0 ? ha[i > 0 ? i - 1 : 0][j] : hs[j];
-                if (first) hp = state_of(a.h0, r, j);
-                dh[j] = fmaf(C, dy, dh[j]);
-                y = fmaf(C, ha[i][j], y);
-                v[j] = dh[j] * u;
-                v[NS + j] = dy * ha[i][j];
-                p = fmaf(dh[j], B, p);
-                dh[j] *= ea[i][j];
-                const float w = dh[j] * hp;
-                dA[j] = fmaf(w, dt, dA[j]);
-                q = fmaf(w, A2[j], q);
-            }
-            if (first) {
-                const SeqRange sr = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + r);
-#pragma unroll
-                for (int j = 0; j < NS; ++j) {
-                    const int n = s * NS + j;
-                    if (a.dh0 != nullptr && live && n < a.N) a.dh0[((long long)sr.q * a.D + d) * a.N + n] = dh[j];
-                    dh[j] = 0.f;
-                }
-            }
-            // dB, dC over the warp's channels
-            int cnt = V;
-#pragma unroll
-            for (int m = 16; m >= S; m >>= 1) {
-                if (cnt > 1) {
-                    cnt /= 2;
-                    const bool up = lane & m;
-#pragma unroll
-                    for (int k = 0; k < cnt; ++k) {
-                        const float keep = up ? v[k + cnt] : v[k], send = up ? v[k] : v[k + cnt];
-                        v[k] = keep + __shfl_xor_sync(0xffffffffu, send, m);
-                    }
-                } else {
-                    v[0] += __shfl_xor_sync(0xffffffffu, v[0], m);
-                }
-            }
-            if (writer) {
-#pragma unroll
-                for (int k = 0; k < RV; ++k) {
-                    const int o = off + k;   // 0..NS-1: dB, then dC
-                    red[i * 2 * NP + (o < NS ? s * NS + o : NP + s * NS + o - NS)] = v[k];
-                }
-            }
-            pv[i & 3] = p; qv[i & 3] = q; yv[i & 3] = y;
-            if ((i & 3) == 0) {
-                lane_sum4<S>(pv[0], pv[1], pv[2], pv[3], s, &s_p[ch * LD + r]);
-                lane_sum4<S>(qv[0], qv[1], qv[2], qv[3], s, &s_q[ch * LD + r]);
-                lane_sum4<S>(yv[0], yv[1], yv[2], yv[3], s, &s_y[ch * LD + r]);
-            }
-        }
+    for (long long tile = t0 + (t1 - t0 - 1) / TT * TT; tile >= t0; tile -= TT) {
+        const Events ev = find_events(a, tile, TT);
+        stage<T, CH, TT, LD, ALIGNED, false>(a, cb, tile, ev.in, s_dt, s_x, s_dy);
+        stage_bc<T, TT, NP>(a, cb.g, tile, ev.in, s_B, s_C);
         __syncthreads();
-        for (int k = tid; k < SUB * 2 * NP; k += kThreads) {
-            const int i = k / (2 * NP), w = k % (2 * NP) / NP, n = k % NP, r = sb * SUB + i;
-            if (n >= a.N || r >= rows) continue;
-            float t = 0.f;
-#pragma unroll
-            for (int x = 0; x < kWarps; ++x) t += s_red[((sb & 1) * kWarps + x) * SUB * 2 * NP + k];
-            bcpart[(((long long)blk * a.M + t0 + r) * 2 + w) * a.N + n] = t;
-        }
-    }
-    float* pseg = part + sg * ((long long)a.D * a.N + 2 * a.D);
-    if (live) {
-#pragma unroll
-        for (int j = 0; j < NS; ++j)
-            if (s * NS + j < a.N) pseg[(long long)d * a.N + s * NS + j] = dA[j];
-    }
-    __syncthreads();
-
-    // rows and channels as they were staged: dx, ddelta, dz; dDskip and the bias' gradient
-    const int c0 = (tid % VPR) * 8, cn = max(0, min(8, cb.n - c0)), dd = cb.d0 + c0;
-    float sD[8] = {}, sb_[8] = {}, dsk[8], bias[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        dsk[i] = i < cn && a.Dskip ? a.Dskip[dd + i] : 0.f;
-        bias[i] = i < cn && a.delta_bias ? a.delta_bias[dd + i] : 0.f;
-    }
 #pragma unroll 1
-    for (int row = tid / VPR; row < L; row += RPP) {
-        if (!bit(ev.in, row) || cn == 0) continue;
-        const long long t = t0 + row;
-        float v[8], dx[8], dv[8];
-        unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.delta) + t * a.ds + dd, cn), v);
+        for (int i0 = TT - kSub; i0 >= 0; i0 -= kSub) {
+            if (tile + i0 >= t1) continue;
+            const long long r8 = (tile + i0) / kSub;
+            F2 hs[2][2];   // the state in front of these rows
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int at = (c0 + i) * LD + row;
-            const float dt = s_dt[at], x = s_x[at], dy = s_dy[at], p = s_p[at];
-            dx[i] = fmaf(p, dt, dsk[i] * dy);
-            dv[i] = fmaf(p, x, s_q[at] * (1.0f / kLog2e));
-            if (a.softplus) dv[i] *= sigmoid<false>(v[i] + bias[i]);
-            sD[i] = fmaf(dy, x, sD[i]);
-            sb_[i] += dv[i];
+            for (int k = 0; k < 2; ++k) {
+                const float cum = tile + i0 < reach && at.live[k] ? dtck[r8 * a.D + at.d[k]] : 0.f;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    hs[k][m] = at.load(hck, r8, a.D, k, m);
+                    if (tile + i0 < reach)
+                        hs[k][m] = fma2(ex2(mul2(both(cum), A2[k][m])), at.load(hseg, sg, a.D, k, m), hs[k][m]);
+                }
+            }
+            float* red = s_red + (phase * kWarps + at.warp) * kSub * 2 * NP;
+            auto rows = [&](auto evc) {
+                constexpr bool EV = decltype(evc)::value;
+                F2 ha[kSub][2][2], ea[kSub][2][2];
+#pragma unroll
+                for (int i = 0; i < kSub; i += 4) {
+                    float4 d4[2], x4[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[at.ch[k] * LD + i0 + i]);
+                        x4[k] = *reinterpret_cast<const float4*>(&s_x[at.ch[k] * LD + i0 + i]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int r = i + j;
+                        SeqRange sr{0, 0, 0, false};
+                        const bool first = EV && (ev.first >> (i0 + r) & 1);
+                        if (first) sr = find_seq(a.cu, a.num_seqs, a.M, a.T, tile + i0 + r);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            const F2 B = lds_pair(s_B + (i0 + r) * NP + at.n(m));
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float dt = j == 0 ? d4[k].x : j == 1 ? d4[k].y : j == 2 ? d4[k].z : d4[k].w;
+                                const float x = j == 0 ? x4[k].x : j == 1 ? x4[k].y : j == 2 ? x4[k].z : x4[k].w;
+                                F2 hp = r > 0 ? ha[r > 0 ? r - 1 : 0][k][m] : hs[k][m];
+                                if (first) hp = at.get(a.h0, sr.q, a, k, m);
+                                ea[r][k][m] = ex2(mul2(both(dt), A2[k][m]));
+                                ha[r][k][m] = fma2(ea[r][k][m], hp, mul2(both(dt * x), B));
+                            }
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = kSub - 4; i >= 0; i -= 4) {
+                    float4 d4[2], x4[2], g4[2];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[at.ch[k] * LD + i0 + i]);
+                        x4[k] = *reinterpret_cast<const float4*>(&s_x[at.ch[k] * LD + i0 + i]);
+                        g4[k] = *reinterpret_cast<const float4*>(&s_dy[at.ch[k] * LD + i0 + i]);
+                    }
+                    float pv[2][4], qv[2][4], yv[2][4];
+#pragma unroll
+                    for (int j = 3; j >= 0; --j) {
+                        const int r = i + j;
+                        const bool first = EV && (ev.first >> (i0 + r) & 1), last = EV && (ev.last >> (i0 + r) & 1);
+                        SeqRange sr{0, 0, 0, false};
+                        if (first || last) sr = find_seq(a.cu, a.num_seqs, a.M, a.T, tile + i0 + r);
+                        F2 B[2], C[2], dB[2], dC[2];
+#pragma unroll
+                        for (int m = 0; m < 2; ++m) {
+                            B[m] = lds_pair(s_B + (i0 + r) * NP + at.n(m));
+                            C[m] = lds_pair(s_C + (i0 + r) * NP + at.n(m));
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float dt = j == 0 ? d4[k].x : j == 1 ? d4[k].y : j == 2 ? d4[k].z : d4[k].w;
+                            const float x = j == 0 ? x4[k].x : j == 1 ? x4[k].y : j == 2 ? x4[k].z : x4[k].w;
+                            const float dy = j == 0 ? g4[k].x : j == 1 ? g4[k].y : j == 2 ? g4[k].z : g4[k].w;
+                            const F2 u = both(dt * x);
+                            F2 p{0.f, 0.f}, q{0.f, 0.f}, y{0.f, 0.f};
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                F2 hp = r > 0 ? ha[r > 0 ? r - 1 : 0][k][m] : hs[k][m];
+                                if (first) hp = at.get(a.h0, sr.q, a, k, m);
+                                if (last) dh[k][m] = at.get(a.d_hT, sr.q, a, k, m);
+                                dh[k][m] = fma2(C[m], both(dy), dh[k][m]);
+                                y = m ? fma2(C[m], ha[r][k][m], y) : mul2(C[m], ha[r][k][m]);
+                                dB[m] = k ? fma2(dh[k][m], u, dB[m]) : mul2(dh[k][m], u);
+                                dC[m] = k ? fma2(ha[r][k][m], both(dy), dC[m]) : mul2(ha[r][k][m], both(dy));
+                                p = m ? fma2(dh[k][m], B[m], p) : mul2(dh[k][m], B[m]);
+                                dh[k][m] = mul2(dh[k][m], ea[r][k][m]);
+                                const F2 w = mul2(dh[k][m], hp);
+                                dA[k][m] = fma2(w, both(dt), dA[k][m]);
+                                q = m ? fma2(w, A2[k][m], q) : mul2(w, A2[k][m]);
+                                if (first) {
+                                    at.put(a.dh0, sr.q, a, k, m, dh[k][m]);
+                                    dh[k][m] = F2{0.f, 0.f};
+                                }
+                            }
+                            pv[k][j] = p.x + p.y;
+                            qv[k][j] = q.x + q.y;
+                            yv[k][j] = y.x + y.y;
+                        }
+                        channel_sum<S>(at, dB, dC, red + r * 2 * NP);
+                    }
+                    lane_sum42<S, LD>(at, pv, s_p + i0 + i);
+                    lane_sum42<S, LD>(at, qv, s_q + i0 + i);
+                    lane_sum42<S, LD>(at, yv, s_y + i0 + i);
+                }
+            };
+            if ((ev.first | ev.last) >> i0 & 0xff) rows(std::true_type{});
+            else rows(std::false_type{});
+            __syncthreads();
+            for (int k = tid; k < kSub * 2 * NP; k += kThreads) {
+                const int r = k / (2 * NP), w = k % (2 * NP) / NP, n = k % NP;
+                if (n >= a.N || tile + i0 + r >= a.M) continue;
+                float t = 0.f;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) t += s_red[(phase * kWarps + x) * kSub * 2 * NP + k];
+                bcpart[(((long long)blk * a.M + tile + i0 + r) * 2 + w) * a.N + n] = t;
+            }
+            phase ^= 1;
         }
-        store8<T, ALIGNED>(static_cast<T*>(a.dx) + t * a.D + dd, dx, cn);
-        store8<T, ALIGNED>(static_cast<T*>(a.ddelta) + t * a.D + dd, dv, cn);
-        if (a.z != nullptr) {
-            float z[8], g[8];
-            unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.z) + t * a.zs + dd, cn), z);
-            unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.d_out) + t * a.D + dd, cn), g);
+        // rows and channels as they were staged: dx, ddelta, dz; dDskip and the bias' gradient
+        // (every lane's p, q and y were written before the last barrier)
+#pragma unroll 1
+        for (int slot = tid; slot < TT * VPR; slot += kThreads) {
+            const int row = slot / VPR, c0 = (slot % VPR) * 8;
+            const int cn = max(0, min(8, cb.n - c0)), d = cb.d0 + c0;
+            if (!(ev.in >> row & 1) || cn == 0) continue;
+            const long long t = tile + row;
+            float v[8], dx[8], dv[8], dsk[8];
+            unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.delta) + t * a.ds + d, cn), v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int at = (c0 + i) * LD + row;
-                const float sg1 = sigmoid<sizeof(T) == 2>(z[i]);
-                g[i] *= fmaf(dsk[i], s_x[at], s_y[at]) * sg1 * fmaf(z[i], 1.0f - sg1, 1.0f);
+                const int o = (c0 + i) * LD + row;
+                const float dt = s_dt[o], x = s_x[o], dy = s_dy[o], p = s_p[o];
+                dsk[i] = a.Dskip && i < cn ? __ldg(a.Dskip + d + i) : 0.f;
+                dx[i] = fmaf(p, dt, dsk[i] * dy);
+                dv[i] = fmaf(p, x, s_q[o] * (1.0f / kLog2e));
+                if (a.softplus) dv[i] *= sigmoid<false>(v[i] + (a.delta_bias && i < cn ? __ldg(a.delta_bias + d + i) : 0.f));
+                sD[i] = fmaf(dy, x, sD[i]);
+                sb[i] += dv[i];
             }
-            store8<T, ALIGNED>(static_cast<T*>(a.dz) + t * a.D + dd, g, cn);
+            store8<T, ALIGNED>(static_cast<T*>(a.dx) + t * a.D + d, dx, cn);
+            store8<T, ALIGNED>(static_cast<T*>(a.ddelta) + t * a.D + d, dv, cn);
+            if (a.z != nullptr) {
+                float z[8], g[8];
+                unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.z) + t * a.zs + d, cn), z);
+                unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.d_out) + t * a.D + d, cn), g);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int o = (c0 + i) * LD + row;
+                    const float sg1 = sigmoid<sizeof(T) == 2>(z[i]);
+                    g[i] *= fmaf(dsk[i], s_x[o], s_y[o]) * sg1 * fmaf(z[i], 1.0f - sg1, 1.0f);
+                }
+                store8<T, ALIGNED>(static_cast<T*>(a.dz) + t * a.D + d, g, cn);
+            }
         }
+        __syncthreads();   // the next tile is laid over this one
     }
-    __syncthreads();
-    // over the rows: RPP partial sums per channel, in the staging area (2 RPP <= 2 L columns)
+    // part[segment]: dA [D][N], dDskip [D], the bias' gradient [D]
+    float* pseg = part + sg * ((long long)a.D * a.N + 2 * a.D);
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) at.put(pseg, 0, a, k, m, dA[k][m]);
+    // over the rows: a thread's slots all have the same channels; RPP partial sums per channel
+    constexpr int RPP = kThreads / VPR > 0 ? kThreads / VPR : 1;
     float* s0 = sm;   // [2][RPP][CH]
+    static_assert(VPR <= kThreads && sizeof(float) * 2 * RPP * CH <= grad_smem<T, S>(), "shared memory holds the partial sums");
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        s0[(tid / VPR) * CH + c0 + i] = sD[i];
-        s0[(RPP + tid / VPR) * CH + c0 + i] = sb_[i];
+        s0[(tid / VPR) * CH + (tid % VPR) * 8 + i] = sD[i];
+        s0[(RPP + tid / VPR) * CH + (tid % VPR) * 8 + i] = sb[i];
     }
     __syncthreads();
     for (int k = tid; k < 2 * CH; k += kThreads) {
@@ -500,72 +639,85 @@ __global__ void __launch_bounds__(256) ssm_bwd_bc_kernel(SsmArgs a, int per, con
 }
 
 struct Layout {
-    long long K;      // segments
+    Segments seg;
     int nblk, per;    // channel blocks in all, per group
-    size_t hseg, rseg, dtseg, part, bcpart, flags, bytes;
+    size_t hseg, rseg, dtseg, hck, dtck, part, bcpart, flags, bytes;
 };
-int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
+// Lanes per channel pair (four states per lane).
+int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
+// Segments of 32 to 256 rows: the longest that still give four CTAs per SM.  Every segment
+// costs a state, a state gradient and a partial sum of dA.
 Layout layout(long long M, int D, int N, int G) {
     Layout l;
-    const int S = lanes_of(N), L = S >= 4 ? 64 : 32, CH = kThreads / S;
-    l.K = (M + L - 1) / L;
+    const int S = lanes_of(N), CH = 2 * kThreads / S;
     l.per = (D / G + CH - 1) / CH;
     l.nblk = l.per * G;
+    l.seg.len = 256;
+    while (l.seg.len > 32 && l.nblk * ((M + l.seg.len - 1) / l.seg.len) < 4LL * kSMs) l.seg.len /= 2;
+    l.seg.count = (M + l.seg.len - 1) / l.seg.len;
+    l.seg.whole = false;
+    const long long K = l.seg.count;
     size_t at = 0;
     auto take = [&](size_t n) { const size_t o = at; at += (n + 255) / 256 * 256; return o; };
-    const size_t dn = (size_t)D * N;
-    l.hseg = take(sizeof(float) * l.K * dn);
-    l.rseg = take(sizeof(float) * l.K * dn);
-    l.dtseg = take(sizeof(float) * l.K * D);
-    l.part = take(sizeof(float) * (l.K > 0 ? l.K : 1) * (dn + 2 * D));
+    const size_t dn = (size_t)D * N, dnp = (size_t)D * 4 * S;
+    l.hseg = take(sizeof(float) * K * dnp);
+    l.rseg = take(sizeof(float) * K * dnp);
+    l.dtseg = take(sizeof(float) * K * D);
+    l.hck = take(sizeof(float) * ((M + kSub - 1) / kSub) * dnp);
+    l.dtck = take(sizeof(float) * ((M + kSub - 1) / kSub) * D);
+    l.part = take(sizeof(float) * (K > 0 ? K : 1) * (dn + 2 * D));
     l.bcpart = take(sizeof(float) * l.nblk * M * 2 * N);
-    l.flags = take(l.K);
+    l.flags = take(K);
     l.bytes = at;
     return l;
 }
 
-template <typename T, int S, int NS, int SUB, bool ALIGNED>
+template <typename T, int S, bool ALIGNED>
 cudaError_t go(const SsmArgs& a, cudaStream_t s) {
     const Layout l = layout(a.M, a.D, a.N, a.G);
+    const long long K = l.seg.count;
     float* hseg = reinterpret_cast<float*>(a.ws + l.hseg);
     float* rseg = reinterpret_cast<float*>(a.ws + l.rseg);
     float* dtseg = reinterpret_cast<float*>(a.ws + l.dtseg);
+    float* hck = reinterpret_cast<float*>(a.ws + l.hck);
+    float* dtck = reinterpret_cast<float*>(a.ws + l.dtck);
     float* part = reinterpret_cast<float*>(a.ws + l.part);
     float* bcpart = reinterpret_cast<float*>(a.ws + l.bcpart);
     uint8_t* flags = a.ws + l.flags;
     const long long extra = a.cu != nullptr || a.T == 0 ? (a.num_seqs < 64 ? a.num_seqs : 64) : 0;
-    const long long dn = (long long)a.D * a.N, bc = a.M * a.G * 2 * a.N;
-    if (l.nblk * (l.K + extra) > 0x7fffffffLL || (bc + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    constexpr int CH = kThreads / S, L = seg_rows<S>(), LD = L + 4, NP = S * NS;
-    constexpr size_t sm1 = sizeof(float) * (3 * CH * LD + 2 * L * NP), sm2 = grad_smem<S, NS, SUB>();
+    const long long dn = (long long)a.D * a.N, dnp = (long long)a.D * 4 * S, bc = a.M * a.G * 2 * a.N;
+    if (l.nblk * (K + extra) > 0x7fffffffLL || (bc + 255) / 256 > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    constexpr size_t sm1 = summary_smem<T, S>(), sm3 = grad_smem<T, S>();
     cudaError_t e = cudaSuccess;
-    if (l.K + extra > 0) {
-        auto k1 = ssm_bwd_summary_kernel<T, S, NS, ALIGNED>;
+    if (K + extra > 0) {
+        auto k1 = ssm_bwd_summary_kernel<T, S, ALIGNED>;
         if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm1)) != cudaSuccess) return e;
-        k1<<<(unsigned)(l.nblk * (l.K + extra)), kThreads, sm1, s>>>(a, l.K, l.nblk, hseg, rseg, dtseg, flags);
+        k1<<<(unsigned)(l.nblk * (K + extra)), kThreads, sm1, s>>>(a, l.seg, l.nblk, hseg, rseg, dtseg, hck, dtck, flags);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    if (l.K > 0) {
-        ssm_bwd_join_kernel<<<dim3((unsigned)((dn + 127) / 128), 2), 128, 0, s>>>(a, l.K, hseg, rseg, dtseg, flags);
+    if (K > 0) {
+        ssm_bwd_join_kernel<<<dim3((unsigned)((dnp + 127) / 128), 2), 128, 0, s>>>(a, 4 * S, K, hseg, rseg, dtseg, flags);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        auto k3 = ssm_bwd_grad_kernel<T, S, NS, SUB, ALIGNED>;
-        if ((e = cudaFuncSetAttribute(k3, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm2)) != cudaSuccess) return e;
-        k3<<<(unsigned)(l.nblk * l.K), kThreads, sm2, s>>>(a, l.K, l.nblk, hseg, rseg, part, bcpart);
+        auto k3 = ssm_bwd_grad_kernel<T, S, ALIGNED>;
+        if ((e = cudaFuncSetAttribute(k3, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm3)) != cudaSuccess) return e;
+        k3<<<(unsigned)(l.nblk * K), kThreads, sm3, s>>>(a, l.seg, l.nblk, hseg, rseg, hck, dtck, part, bcpart);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         ssm_bwd_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(a, l.per, bcpart);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
-    return launch_colsum(part, (int)l.K, dn, a.dA, a.D, a.dDskip, a.D, a.ddelta_bias, s);
+    return launch_colsum(part, (int)K, dn, a.dA, a.D, a.dDskip, a.D, a.ddelta_bias, s);
 }
 
 template <typename T, bool ALIGNED>
 cudaError_t go_n(const SsmArgs& a, cudaStream_t s) {
-    if (a.N <= 4) return go<T, 1, 4, 8, ALIGNED>(a, s);
-    if (a.N <= 8) return go<T, 2, 4, 8, ALIGNED>(a, s);
-    if (a.N <= 16) return go<T, 4, 4, 8, ALIGNED>(a, s);
-    if (a.N <= 32) return go<T, 8, 4, 8, ALIGNED>(a, s);
-    if (a.N <= 64) return go<T, 16, 4, 8, ALIGNED>(a, s);
-    return go<T, 16, 8, 4, ALIGNED>(a, s);
+    switch (lanes_of(a.N)) {
+        case 1: return go<T, 1, ALIGNED>(a, s);
+        case 2: return go<T, 2, ALIGNED>(a, s);
+        case 4: return go<T, 4, ALIGNED>(a, s);
+        case 8: return go<T, 8, ALIGNED>(a, s);
+        case 16: return go<T, 16, ALIGNED>(a, s);
+        default: return go<T, 32, ALIGNED>(a, s);
+    }
 }
 
 template <typename T>
