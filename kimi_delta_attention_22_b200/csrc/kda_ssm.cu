@@ -129,11 +129,14 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
                 unpack<T, 8>(nx, x);
                 unpack<T, 8>(nd, v);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    v[i] += bias[i];
-                    if (a.softplus) v[i] = softplus(v[i]);
-                    s_dt[(sc0 + i) * LD + srow] = v[i];
-                    s_u[(sc0 + i) * LD + srow] = v[i] * x[i];
+                for (int i = 0; i < 8; i += 2) {
+                    F2 dt = add2(F2{v[i], v[i + 1]}, F2{bias[i], bias[i + 1]});
+                    if (a.softplus) dt = softplus2(dt);
+                    const F2 u = mul2(dt, F2{x[i], x[i + 1]});
+                    s_dt[(sc0 + i) * LD + srow] = dt.x;
+                    s_dt[(sc0 + i + 1) * LD + srow] = dt.y;
+                    s_u[(sc0 + i) * LD + srow] = u.x;
+                    s_u[(sc0 + i + 1) * LD + srow] = u.y;
                 }
             }
 #pragma unroll
@@ -158,9 +161,15 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
                 unpack<T, 8>(cx, x);
                 unpack<T, 8>(cz, z);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    y[i] = fmaf(dsk[i], x[i], s_y[(sc0 + i) * LD + srow]);
-                    if (a.z) y[i] *= z[i] * sigmoid<sizeof(T) == 2>(z[i]);
+                for (int i = 0; i < 8; i += 2) {
+                    F2 o = fma2(F2{dsk[i], dsk[i + 1]}, F2{x[i], x[i + 1]},
+                                F2{s_y[(sc0 + i) * LD + srow], s_y[(sc0 + i + 1) * LD + srow]});
+                    if (a.z) {
+                        const F2 zz{z[i], z[i + 1]};
+                        o = mul2(o, mul2(zz, sigmoid2(zz)));
+                    }
+                    y[i] = o.x;
+                    y[i + 1] = o.y;
                 }
                 store8<T, ALIGNED>(static_cast<T*>(a.out) + (tile + srow) * a.D + sd, y, scn);
             }

@@ -47,23 +47,35 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
 __device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
 __device__ __forceinline__ F2 ex2(F2 v) { return F2{ex2(v.x), ex2(v.y)}; }
 
+__device__ __forceinline__ F2 rcp(F2 v) {
+    F2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    return r;
+}
+
+// The functions of the step size and the gate work on pairs and take the hardware's exponential
+// and reciprocal: each within a few units, |v| log2(e) more through the exponent's rounding.
+__device__ __forceinline__ F2 sigmoid2(F2 v) { return rcp(add2(both(1.0f), ex2(mul2(v, both(-kLog2e))))); }
+
 // softplus(v) = max(v, 0) + log(1 + e), e = e^-|v| <= 1.  With s = e / (2 + e) <= 1/3,
 // log(1 + e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ..): the series ends at s^14/15, whose
 // remainder is below 2e-9 of the sum, so the value keeps its relative accuracy where e is
 // tiny (step sizes of 1e-3 and less), which a logarithm of 1 + e does not.
-__device__ __forceinline__ float softplus(float v) {
-    const float e = ex2(-kLog2e * fabsf(v));
-    const float s = __fdividef(e, 2.0f + e), q = s * s;
-    float p = 1.0f / 15.0f;
-    p = fmaf(p, q, 1.0f / 13.0f);
-    p = fmaf(p, q, 1.0f / 11.0f);
-    p = fmaf(p, q, 1.0f / 9.0f);
-    p = fmaf(p, q, 1.0f / 7.0f);
-    p = fmaf(p, q, 1.0f / 5.0f);
-    p = fmaf(p, q, 1.0f / 3.0f);
-    p = fmaf(p, q, 1.0f);
-    return fmaf(2.0f * s, p, fmaxf(v, 0.0f));   // a NaN stays one through e
+__device__ __forceinline__ F2 softplus2(F2 v) {
+    const F2 e = ex2(mul2(F2{fabsf(v.x), fabsf(v.y)}, both(-kLog2e)));
+    const F2 s = mul2(e, rcp(add2(e, both(2.0f)))), q = mul2(s, s);
+    F2 p = both(1.0f / 15.0f);
+    p = fma2(p, q, both(1.0f / 13.0f));
+    p = fma2(p, q, both(1.0f / 11.0f));
+    p = fma2(p, q, both(1.0f / 9.0f));
+    p = fma2(p, q, both(1.0f / 7.0f));
+    p = fma2(p, q, both(1.0f / 5.0f));
+    p = fma2(p, q, both(1.0f / 3.0f));
+    p = fma2(p, q, both(1.0f));
+    return fma2(add2(s, s), p, F2{fmaxf(v.x, 0.0f), fmaxf(v.y, 0.0f)});   // a NaN stays one through e
 }
+__device__ __forceinline__ float softplus(float v) { return softplus2(F2{v, v}).x; }
 
 // 8 consecutive channels of one row (those below `n`), as raw words.
 template <typename T, bool ALIGNED>

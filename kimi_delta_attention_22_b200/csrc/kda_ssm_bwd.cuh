@@ -1,4 +1,4 @@
-// kda_ssm_bwd.cu -- gradients of the selective state space scan.
+// kda_ssm_bwd.cuh -- gradients of the selective state space scan.
 //
 // With dy = d_out silu(z) and, from the last row of a sequence back,
 //     dh[n]  <- dh[n] + C[n] dy                       (dh starts from d_hT)
@@ -31,6 +31,8 @@
 // keeps one half of its values and sends the other.  Where the halves are register pairs or
 // channels, lanes on the upper side hold them in swapped order, so that every lane keeps the
 // same registers and nothing is selected.
+#pragma once
+
 #include <type_traits>
 
 #include "kda_ssm.cuh"
@@ -41,12 +43,21 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kSub = 8;        // rows between checkpoints
+constexpr int kSub = 4;        // rows between checkpoints
 
 template <int S>
 constexpr int channels() { return 2 * kThreads / S; }
 template <int S>
 constexpr int tile_rows() { return S >= 4 ? 32 : 8 * S; }
+
+// Where row `row` of channel c lies in a tile array [channel][row]: groups of four rows stay
+// together (one 16-byte access) and are permuted by the channel, so that neither the staging
+// threads (the same channel of eight vectors, four rows) nor the scanning ones (eight
+// neighbouring channels, the same rows) meet in a bank.
+template <int TT>
+__device__ __forceinline__ int cell(int c, int row) {
+    return c * TT + ((((row >> 2) ^ (c >> 3) ^ c) & (TT / 4 - 1)) << 2 | (row & 3));
+}
 
 // First / last rows of sequences and rows of any sequence, one bit per row of the tile.
 struct Events {
@@ -78,7 +89,7 @@ __device__ __forceinline__ F2 shfl2(F2 v, int m) {
 
 // dt, x (or dt x) and dy of the tile into shared memory [channel][row]; zeros in rows
 // that no sequence covers, which then neither decay nor add anything.
-template <typename T, int CH, int TT, int LD, bool ALIGNED, bool TIMES>
+template <typename T, int CH, int TT, bool ALIGNED, bool TIMES>
 __device__ __forceinline__ void stage(const SsmArgs& a, const ChannelBlock& cb, long long t0, uint32_t in, float* s_dt,
                                       float* s_x, float* s_dy) {
     constexpr int VPR = CH / 8;
@@ -101,16 +112,27 @@ __device__ __forceinline__ void stage(const SsmArgs& a, const ChannelBlock& cb, 
             float z[8];
             unpack<T, 8>(pz, z);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] *= z[i] * sigmoid<sizeof(T) == 2>(z[i]);
+            for (int i = 0; i < 8; i += 2) {
+                const F2 zz{z[i], z[i + 1]}, o = mul2(F2{g[i], g[i + 1]}, mul2(zz, sigmoid2(zz)));
+                g[i] = o.x;
+                g[i + 1] = o.y;
+            }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (a.delta_bias && i < n) v[i] += __ldg(a.delta_bias + d + i);
-            if (a.softplus) v[i] = softplus(v[i]);
-            if (i >= n) v[i] = 0.f;
-            s_dt[(c0 + i) * LD + row] = v[i];
-            s_x[(c0 + i) * LD + row] = TIMES ? v[i] * x[i] : x[i];
-            s_dy[(c0 + i) * LD + row] = g[i];
+        for (int i = 0; i < 8; i += 2) {
+            F2 dt{v[i], v[i + 1]};
+            if (a.delta_bias) dt = add2(dt, F2{i < n ? __ldg(a.delta_bias + d + i) : 0.f, i + 1 < n ? __ldg(a.delta_bias + d + i + 1) : 0.f});
+            if (a.softplus) dt = softplus2(dt);
+            if (i >= n) dt.x = 0.f;
+            if (i + 1 >= n) dt.y = 0.f;
+            const F2 xx = TIMES ? mul2(dt, F2{x[i], x[i + 1]}) : F2{x[i], x[i + 1]};
+            const int o = cell<TT>(c0 + i, row), o2 = cell<TT>(c0 + i + 1, row);
+            s_dt[o] = dt.x;
+            s_dt[o2] = dt.y;
+            s_x[o] = xx.x;
+            s_x[o2] = xx.y;
+            s_dy[o] = g[i];
+            s_dy[o2] = g[i + 1];
         }
     }
 }
@@ -183,17 +205,17 @@ struct Place {
 
 template <typename T, int S>
 constexpr size_t summary_smem() {
-    return sizeof(float) * 3 * channels<S>() * (tile_rows<S>() + 4) + sizeof(T) * 2 * tile_rows<S>() * 4 * S;
+    return sizeof(float) * 3 * channels<S>() * tile_rows<S>() + sizeof(T) * 2 * tile_rows<S>() * 4 * S;
 }
 
 template <typename T, int S, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a, Segments seg, int nblk, float* hseg,
                                                                      float* rseg, float* dtseg, float* hck, float* dtck,
                                                                      uint8_t* flags) {
-    constexpr int CH = channels<S>(), TT = tile_rows<S>(), LD = TT + 4, NP = 4 * S;
+    constexpr int CH = channels<S>(), TT = tile_rows<S>(), NP = 4 * S;
     extern __shared__ __align__(16) float sm[];
-    float *s_dt = sm, *s_u = s_dt + CH * LD, *s_dy = s_u + CH * LD;
-    T *s_B = reinterpret_cast<T*>(s_dy + CH * LD), *s_C = s_B + TT * NP;
+    float *s_dt = sm, *s_u = s_dt + CH * TT, *s_dy = s_u + CH * TT;
+    T *s_B = reinterpret_cast<T*>(s_dy + CH * TT), *s_C = s_B + TT * NP;
     const long long sg = blockIdx.x / nblk;
     const ChannelBlock cb = channel_block<CH>(blockIdx.x % nblk, a.D, a.G);
     const Place<S> at(cb);
@@ -227,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
         if (ev.first) f |= kStarts;
         if (ev.last) f |= kEnds;
         if (tile != t0) __syncthreads();
-        stage<T, CH, TT, LD, ALIGNED, true>(a, cb, tile, ev.in, s_dt, s_u, s_dy);
+        stage<T, CH, TT, ALIGNED, true>(a, cb, tile, ev.in, s_dt, s_u, s_dy);
         stage_bc<T, TT, NP>(a, cb.g, tile, ev.in, s_B, s_C);
         __syncthreads();
 #pragma unroll 1
@@ -247,9 +269,9 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
                     float4 d4[2], u4[2], g4[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[at.ch[k] * LD + i]);
-                        u4[k] = *reinterpret_cast<const float4*>(&s_u[at.ch[k] * LD + i]);
-                        g4[k] = *reinterpret_cast<const float4*>(&s_dy[at.ch[k] * LD + i]);
+                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[cell<TT>(at.ch[k], i)]);
+                        u4[k] = *reinterpret_cast<const float4*>(&s_u[cell<TT>(at.ch[k], i)]);
+                        g4[k] = *reinterpret_cast<const float4*>(&s_dy[cell<TT>(at.ch[k], i)]);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -291,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
                     }
                 }
             };
-            if ((ev.first | ev.last) >> i0 & 0xff) rows(std::true_type{});
+            if ((ev.first | ev.last) >> i0 & ((1u << kSub) - 1)) rows(std::true_type{});
             else rows(std::false_type{});
         }
     }
@@ -345,25 +367,25 @@ __global__ void __launch_bounds__(128) ssm_bwd_join_kernel(SsmArgs a, int NP, lo
 }
 
 // The sums over a channel's S lanes of four rows' values v[slot][row], written to
-// to[channel * LD + row]: channels are exchanged first (in swapped order), then rows.
-template <int S, int LD>
-__device__ __forceinline__ void lane_sum42(const Place<S>& at, float (&v)[2][4], float* to) {
+// the channel's cell of `row` (a multiple of 4): channels are exchanged first (in swapped order), then rows.
+template <int S, int TT>
+__device__ __forceinline__ void lane_sum42(const Place<S>& at, float (&v)[2][4], float* to, int row) {
     if constexpr (S == 1) {
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(to + at.ch[k] * LD) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
+            *reinterpret_cast<float4*>(to + cell<TT>(at.ch[k], row)) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
     } else {
         F2 lo = add2(F2{v[0][0], v[0][1]}, shfl2(F2{v[1][0], v[1][1]}, 1));
         F2 hi = add2(F2{v[0][2], v[0][3]}, shfl2(F2{v[1][2], v[1][3]}, 1));
         if constexpr (S == 2) {
-            *reinterpret_cast<float4*>(to + at.ch[0] * LD) = make_float4(lo.x, lo.y, hi.x, hi.y);
+            *reinterpret_cast<float4*>(to + cell<TT>(at.ch[0], row)) = make_float4(lo.x, lo.y, hi.x, hi.y);
         } else {
             const bool up = at.s & 2;   // keeps rows 2 and 3
             F2 keep = up ? hi : lo;
             keep = add2(keep, shfl2(up ? lo : hi, 2));
 #pragma unroll
             for (int m = 4; m < S; m <<= 1) keep = add2(keep, shfl2(keep, m));
-            if (at.s < 4) *reinterpret_cast<float2*>(to + at.ch[0] * LD + (up ? 2 : 0)) = make_float2(keep.x, keep.y);
+            if (at.s < 4) *reinterpret_cast<float2*>(to + cell<TT>(at.ch[0], row) + (up ? 2 : 0)) = make_float2(keep.x, keep.y);
         }
     }
 }
@@ -399,21 +421,33 @@ __device__ __forceinline__ void channel_sum(const Place<S>& at, const F2 (&dB)[2
     }
 }
 
+// Asynchronous copies of a thread's own checkpoint (8 floats, two sums of dt) into its slots
+// of shared memory, one checkpoint ahead of its use.
+__device__ __forceinline__ void cp_async8(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+constexpr int kCk = 10 * kThreads;   // [4 pairs][thread] of float2, then [2][thread]
+
 template <typename T, int S>
 constexpr size_t grad_smem() {
-    return sizeof(float) * (6 * channels<S>() * (tile_rows<S>() + 4) + 2 * kWarps * kSub * 2 * 4 * S) +
+    return sizeof(float) * (6 * channels<S>() * tile_rows<S>() + 2 * kWarps * kSub * 2 * 4 * S + 3 * kCk) +
            sizeof(T) * 2 * tile_rows<S>() * 4 * S;
 }
 
 template <typename T, int S, bool ALIGNED>
-__global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(SsmArgs a, Segments seg, int nblk, const float* hseg,
+__global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Segments seg, int nblk, const float* hseg,
                                                                   const float* rseg, const float* hck, const float* dtck,
                                                                   float* part, float* bcpart) {
-    constexpr int CH = channels<S>(), TT = tile_rows<S>(), LD = TT + 4, NP = 4 * S, VPR = CH / 8;
+    constexpr int CH = channels<S>(), TT = tile_rows<S>(), NP = 4 * S, VPR = CH / 8;
     extern __shared__ __align__(16) float sm[];
-    float *s_dt = sm, *s_x = s_dt + CH * LD, *s_dy = s_x + CH * LD;
-    float *s_p = s_dy + CH * LD, *s_q = s_p + CH * LD, *s_y = s_q + CH * LD, *s_red = s_y + CH * LD;
-    T *s_B = reinterpret_cast<T*>(s_red + 2 * kWarps * kSub * 2 * NP), *s_C = s_B + TT * NP;
+    float *s_dt = sm, *s_x = s_dt + CH * TT, *s_dy = s_x + CH * TT;
+    float *s_p = s_dy + CH * TT, *s_q = s_p + CH * TT, *s_y = s_q + CH * TT, *s_red = s_y + CH * TT;
+    float* s_ck = s_red + 2 * kWarps * kSub * 2 * NP;   // two checkpoints, then the segment's incoming state
+    T *s_B = reinterpret_cast<T*>(s_ck + 3 * kCk), *s_C = s_B + TT * NP;
     const long long sg = blockIdx.x / nblk;
     const int blk = blockIdx.x % nblk, tid = threadIdx.x;
     const ChannelBlock cb = channel_block<CH>(blk, a.D, a.G);
@@ -432,29 +466,56 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(SsmArgs a, Se
             dh[k][m] = at.load(rseg, sg, a.D, k, m);
             dA[k][m] = F2{0.f, 0.f};
         }
+    auto slot = [&](int which, int k, int m) { return s_ck + which * kCk + ((k * 2 + m) * kThreads + tid) * 2; };
+    auto slot_dt = [&](int which, int k) { return s_ck + which * kCk + 8 * kThreads + k * kThreads + tid; };
+    auto fetch = [&](long long row, int which) {   // the checkpoint in front of `row`
+        const long long r8 = row / kSub;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            if (!at.live[k]) continue;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) cp_async8(slot(which, k, m), hck + (r8 * a.D + at.d[k]) * NP + at.n(m));
+            cp_async4(slot_dt(which, k), dtck + r8 * a.D + at.d[k]);
+        }
+    };
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const F2 v = at.load(hseg, sg, a.D, k, m), z{0.f, 0.f};
+            *reinterpret_cast<float2*>(slot(2, k, m)) = make_float2(v.x, v.y);
+            if (!at.live[k])
+                for (int w = 0; w < 2; ++w) {
+                    *reinterpret_cast<float2*>(slot(w, k, m)) = make_float2(z.x, z.y);
+                    *slot_dt(w, k) = 0.f;
+                }
+        }
+    fetch((t1 - 1) / kSub * kSub, 0);
     float sD[8] = {}, sb[8] = {};
     int phase = 0;
 
     for (long long tile = t0 + (t1 - t0 - 1) / TT * TT; tile >= t0; tile -= TT) {
         const Events ev = find_events(a, tile, TT);
-        stage<T, CH, TT, LD, ALIGNED, false>(a, cb, tile, ev.in, s_dt, s_x, s_dy);
+        stage<T, CH, TT, ALIGNED, false>(a, cb, tile, ev.in, s_dt, s_x, s_dy);
         stage_bc<T, TT, NP>(a, cb.g, tile, ev.in, s_B, s_C);
         __syncthreads();
 #pragma unroll 1
         for (int i0 = TT - kSub; i0 >= 0; i0 -= kSub) {
             if (tile + i0 >= t1) continue;
-            const long long r8 = (tile + i0) / kSub;
             F2 hs[2][2];   // the state in front of these rows
+            cp_async_wait();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float cum = tile + i0 < reach && at.live[k] ? dtck[r8 * a.D + at.d[k]] : 0.f;
+            for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
-                    hs[k][m] = at.load(hck, r8, a.D, k, m);
-                    if (tile + i0 < reach)
-                        hs[k][m] = fma2(ex2(mul2(both(cum), A2[k][m])), at.load(hseg, sg, a.D, k, m), hs[k][m]);
+                    const float2 v = *reinterpret_cast<const float2*>(slot(phase, k, m));
+                    hs[k][m] = F2{v.x, v.y};
+                    if (tile + i0 < reach) {
+                        const float2 in = *reinterpret_cast<const float2*>(slot(2, k, m));
+                        hs[k][m] = fma2(ex2(mul2(both(*slot_dt(phase, k)), A2[k][m])), F2{in.x, in.y}, hs[k][m]);
+                    }
                 }
-            }
+            if (tile + i0 > t0) fetch(tile + i0 - kSub, phase ^ 1);
             float* red = s_red + (phase * kWarps + at.warp) * kSub * 2 * NP;
             auto rows = [&](auto evc) {
                 constexpr bool EV = decltype(evc)::value;
@@ -464,8 +525,8 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(SsmArgs a, Se
                     float4 d4[2], x4[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[at.ch[k] * LD + i0 + i]);
-                        x4[k] = *reinterpret_cast<const float4*>(&s_x[at.ch[k] * LD + i0 + i]);
+                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[cell<TT>(at.ch[k], i0 + i)]);
+                        x4[k] = *reinterpret_cast<const float4*>(&s_x[cell<TT>(at.ch[k], i0 + i)]);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -493,9 +554,9 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(SsmArgs a, Se
                     float4 d4[2], x4[2], g4[2];
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[at.ch[k] * LD + i0 + i]);
-                        x4[k] = *reinterpret_cast<const float4*>(&s_x[at.ch[k] * LD + i0 + i]);
-                        g4[k] = *reinterpret_cast<const float4*>(&s_dy[at.ch[k] * LD + i0 + i]);
+                        d4[k] = *reinterpret_cast<const float4*>(&s_dt[cell<TT>(at.ch[k], i0 + i)]);
+                        x4[k] = *reinterpret_cast<const float4*>(&s_x[cell<TT>(at.ch[k], i0 + i)]);
+                        g4[k] = *reinterpret_cast<const float4*>(&s_dy[cell<TT>(at.ch[k], i0 + i)]);
                     }
                     float pv[2][4], qv[2][4], yv[2][4];
 #pragma unroll
@@ -542,12 +603,12 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(SsmArgs a, Se
                         }
                         channel_sum<S>(at, dB, dC, red + r * 2 * NP);
                     }
-                    lane_sum42<S, LD>(at, pv, s_p + i0 + i);
-                    lane_sum42<S, LD>(at, qv, s_q + i0 + i);
-                    lane_sum42<S, LD>(at, yv, s_y + i0 + i);
+                    lane_sum42<S, TT>(at, pv, s_p, i0 + i);
+                    lane_sum42<S, TT>(at, qv, s_q, i0 + i);
+                    lane_sum42<S, TT>(at, yv, s_y, i0 + i);
                 }
             };
-            if ((ev.first | ev.last) >> i0 & 0xff) rows(std::true_type{});
+            if ((ev.first | ev.last) >> i0 & ((1u << kSub) - 1)) rows(std::true_type{});
             else rows(std::false_type{});
             __syncthreads();
             for (int k = tid; k < kSub * 2 * NP; k += kThreads) {
@@ -568,33 +629,44 @@ __global__ void __launch_bounds__(kThreads, 2) ssm_bwd_grad_kernel(SsmArgs a, Se
             const int cn = max(0, min(8, cb.n - c0)), d = cb.d0 + c0;
             if (!(ev.in >> row & 1) || cn == 0) continue;
             const long long t = tile + row;
-            float v[8], dx[8], dv[8], dsk[8];
+            float v[8], dx[8], z[8], g[8];
             unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.delta) + t * a.ds + d, cn), v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int o = (c0 + i) * LD + row;
-                const float dt = s_dt[o], x = s_x[o], dy = s_dy[o], p = s_p[o];
-                dsk[i] = a.Dskip && i < cn ? __ldg(a.Dskip + d + i) : 0.f;
-                dx[i] = fmaf(p, dt, dsk[i] * dy);
-                dv[i] = fmaf(p, x, s_q[o] * (1.0f / kLog2e));
-                if (a.softplus) dv[i] *= sigmoid<false>(v[i] + (a.delta_bias && i < cn ? __ldg(a.delta_bias + d + i) : 0.f));
-                sD[i] = fmaf(dy, x, sD[i]);
-                sb[i] += dv[i];
-            }
-            store8<T, ALIGNED>(static_cast<T*>(a.dx) + t * a.D + d, dx, cn);
-            store8<T, ALIGNED>(static_cast<T*>(a.ddelta) + t * a.D + d, dv, cn);
             if (a.z != nullptr) {
-                float z[8], g[8];
                 unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.z) + t * a.zs + d, cn), z);
                 unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.d_out) + t * a.D + d, cn), g);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int o = (c0 + i) * LD + row;
-                    const float sg1 = sigmoid<sizeof(T) == 2>(z[i]);
-                    g[i] *= fmaf(dsk[i], s_x[o], s_y[o]) * sg1 * fmaf(z[i], 1.0f - sg1, 1.0f);
-                }
-                store8<T, ALIGNED>(static_cast<T*>(a.dz) + t * a.D + d, g, cn);
             }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                const int o = cell<TT>(c0 + i, row), o2 = cell<TT>(c0 + i + 1, row);
+                const F2 dt{s_dt[o], s_dt[o2]}, x{s_x[o], s_x[o2]}, dy{s_dy[o], s_dy[o2]}, p{s_p[o], s_p[o2]};
+                F2 sk{0.f, 0.f};
+                if (a.Dskip) sk = F2{i < cn ? __ldg(a.Dskip + d + i) : 0.f, i + 1 < cn ? __ldg(a.Dskip + d + i + 1) : 0.f};
+                const F2 ox = fma2(p, dt, mul2(sk, dy));
+                F2 ov = fma2(p, x, mul2(F2{s_q[o], s_q[o2]}, both(1.0f / kLog2e)));
+                if (a.softplus) {
+                    F2 raw{v[i], v[i + 1]};
+                    if (a.delta_bias) raw = add2(raw, F2{i < cn ? __ldg(a.delta_bias + d + i) : 0.f, i + 1 < cn ? __ldg(a.delta_bias + d + i + 1) : 0.f});
+                    ov = mul2(ov, sigmoid2(raw));
+                }
+                if (a.z != nullptr) {
+                    const F2 zz{z[i], z[i + 1]}, sg1 = sigmoid2(zz), y = fma2(sk, x, F2{s_y[o], s_y[o2]});
+                    const F2 slope = mul2(sg1, fma2(zz, fma2(sg1, both(-1.0f), both(1.0f)), both(1.0f)));
+                    const F2 oz = mul2(mul2(F2{g[i], g[i + 1]}, y), slope);
+                    z[i] = oz.x;
+                    z[i + 1] = oz.y;
+                }
+                sD[i] = fmaf(dy.x, x.x, sD[i]);
+                sD[i + 1] = fmaf(dy.y, x.y, sD[i + 1]);
+                sb[i] += ov.x;
+                sb[i + 1] += ov.y;
+                dx[i] = ox.x;
+                dx[i + 1] = ox.y;
+                v[i] = ov.x;
+                v[i + 1] = ov.y;
+            }
+            store8<T, ALIGNED>(static_cast<T*>(a.dx) + t * a.D + d, dx, cn);
+            store8<T, ALIGNED>(static_cast<T*>(a.ddelta) + t * a.D + d, v, cn);
+            if (a.z != nullptr) store8<T, ALIGNED>(static_cast<T*>(a.dz) + t * a.D + d, z, cn);
         }
         __syncthreads();   // the next tile is laid over this one
     }
@@ -645,7 +717,8 @@ struct Layout {
 };
 // Lanes per channel pair (four states per lane).
 int lanes_of(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : N <= 64 ? 16 : 32; }
-// Segments of 32 to 256 rows: the longest that still give four CTAs per SM.  Every segment
+// Segments of 32 to 256 rows: the longest that still give twelve CTAs per SM (of which two
+// run at a time: the last turn's idle SMs are then a small share).  Every segment
 // costs a state, a state gradient and a partial sum of dA.
 Layout layout(long long M, int D, int N, int G) {
     Layout l;
@@ -653,7 +726,7 @@ Layout layout(long long M, int D, int N, int G) {
     l.per = (D / G + CH - 1) / CH;
     l.nblk = l.per * G;
     l.seg.len = 256;
-    while (l.seg.len > 32 && l.nblk * ((M + l.seg.len - 1) / l.seg.len) < 4LL * kSMs) l.seg.len /= 2;
+    while (l.seg.len > 32 && l.nblk * ((M + l.seg.len - 1) / l.seg.len) < 12LL * kSMs) l.seg.len /= 2;
     l.seg.count = (M + l.seg.len - 1) / l.seg.len;
     l.seg.whole = false;
     const long long K = l.seg.count;
@@ -732,13 +805,5 @@ cudaError_t go_t(const SsmArgs& a, cudaStream_t s) {
 
 }  // namespace
 }  // namespace ssm
-
-cudaError_t launch_ssm_bwd(const SsmArgs& a, bool bf16, cudaStream_t s) {
-    return bf16 ? ssm::go_t<__nv_bfloat16>(a, s) : ssm::go_t<float>(a, s);
-}
-
-size_t ssm_bwd_workspace_bytes(long long B, long long T, int D, int N, int G) {
-    return ssm::layout(B * T, D, N, G).bytes;
-}
 
 }  // namespace kda
