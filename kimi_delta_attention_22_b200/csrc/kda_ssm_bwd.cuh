@@ -63,14 +63,22 @@ __device__ __forceinline__ int cell(int c, int row) {
 struct Events {
     uint32_t first, last, in;
 };
-__device__ __forceinline__ Events find_events(const SsmArgs& a, long long t0, int rows) {   // whole warps
-    const int i = threadIdx.x & 31;
-    SeqRange r{0, 0, 0, false};
-    if (i < rows && t0 + i < a.M) r = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + i);
+// r: a sequence met before (or none).  A tile inside it needs no search, the common case.
+__device__ __forceinline__ Events find_events(const SsmArgs& a, long long t0, int rows, SeqRange& r) {   // whole warps
     Events e;
-    e.first = __ballot_sync(0xffffffffu, r.ok && r.b == t0 + i);
-    e.last = __ballot_sync(0xffffffffu, r.ok && r.e == t0 + i + 1);
-    e.in = __ballot_sync(0xffffffffu, r.ok);
+    if (!r.ok || t0 < r.b || t0 >= r.e) r = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 < a.M ? t0 : a.M - 1);
+    if (r.ok && t0 >= r.b && t0 + rows <= r.e) {
+        e.in = rows == 32 ? 0xffffffffu : (1u << rows) - 1;
+        e.first = t0 == r.b ? 1u : 0u;
+        e.last = t0 + rows == r.e ? 1u << (rows - 1) : 0u;
+        return e;
+    }
+    const int i = threadIdx.x & 31;
+    SeqRange m{0, 0, 0, false};
+    if (i < rows && t0 + i < a.M) m = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + i);
+    e.first = __ballot_sync(0xffffffffu, m.ok && m.b == t0 + i);
+    e.last = __ballot_sync(0xffffffffu, m.ok && m.e == t0 + i + 1);
+    e.in = __ballot_sync(0xffffffffu, m.ok);
     return e;
 }
 
@@ -87,68 +95,136 @@ __device__ __forceinline__ F2 shfl2(F2 v, int m) {
     return F2{__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m)};
 }
 
-// dt, x (or dt x) and dy of the tile into shared memory [channel][row]; zeros in rows
-// that no sequence covers, which then neither decay nor add anything.
-template <typename T, int CH, int TT, bool ALIGNED, bool TIMES>
-__device__ __forceinline__ void stage(const SsmArgs& a, const ChannelBlock& cb, long long t0, uint32_t in, float* s_dt,
-                                      float* s_x, float* s_dy) {
-    constexpr int VPR = CH / 8;
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {   // zeros unless `on`
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src),
+                 "r"(on ? 16 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async8(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// One tile of the inputs as loaded: a thread's slots of one row and eight channels each, in
+// shared memory that only this thread touches, so that the copies run while the tile before is
+// worked on and need no barrier; and its share of B and C in registers.
+template <typename T, int S, bool ALIGNED>
+struct Raw {
+    static constexpr int CH = channels<S>(), TT = tile_rows<S>(), NP = 4 * S;
+    static constexpr int VPR = CH / 8, NSLOT = (TT * VPR + kThreads - 1) / kThreads;
+    static constexpr int W = sizeof(T) / 2;             // 16-byte words of eight channels
+    static constexpr int kBytes = 4 * NSLOT * W * 16 * kThreads;
+    static constexpr int BPT = TT * NP / kThreads > 0 ? TT * NP / kThreads : 1;
+    static constexpr bool kAhead = BPT <= 8;
+    uint4* at;
+    T nB[kAhead ? BPT : 1], nC[kAhead ? BPT : 1];
+    __device__ __forceinline__ explicit Raw(void* mem) : at(static_cast<uint4*>(mem) + threadIdx.x) {}
+
+    __device__ __forceinline__ void load1(int which, int it, const T* p, int n) {
+        uint4* to = at + (which * NSLOT + it) * W * kThreads;
+        if constexpr (ALIGNED) {
 #pragma unroll
-    for (int it = 0; it < (TT * VPR + kThreads - 1) / kThreads; ++it) {
-        const int slot = it * kThreads + threadIdx.x, row = slot / VPR, c0 = (slot % VPR) * 8;
-        if (row >= TT) break;
-        const int cn = max(0, min(8, cb.n - c0)), d = cb.d0 + c0;
-        const long long t = t0 + row;
-        const int n = in >> row & 1 ? cn : 0;
-        const Pack<T, 8> px = load8<T, ALIGNED>(static_cast<const T*>(a.x) + t * a.xs + d, n);
-        const Pack<T, 8> pv = load8<T, ALIGNED>(static_cast<const T*>(a.delta) + t * a.ds + d, n);
-        const Pack<T, 8> pg = load8<T, ALIGNED>(static_cast<const T*>(a.d_out) + t * a.D + d, n);
-        const Pack<T, 8> pz = a.z ? load8<T, ALIGNED>(static_cast<const T*>(a.z) + t * a.zs + d, n) : zero_pack<T, 8>();
-        float x[8], v[8], g[8];
-        unpack<T, 8>(px, x);
-        unpack<T, 8>(pv, v);
-        unpack<T, 8>(pg, g);
-        if (a.z != nullptr) {
-            float z[8];
-            unpack<T, 8>(pz, z);
+            for (int w = 0; w < W; ++w) cp_async16(to + w * kThreads, n > 0 ? p + w * (16 / sizeof(T)) : p, n > 0);
+        } else {
+            const Pack<T, 8> v = load8<T, false>(p, n);
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                const F2 zz{z[i], z[i + 1]}, o = mul2(F2{g[i], g[i + 1]}, mul2(zz, sigmoid2(zz)));
-                g[i] = o.x;
-                g[i + 1] = o.y;
+            for (int w = 0; w < W; ++w) to[w * kThreads] = make_uint4(v.w[4 * w], v.w[4 * w + 1], v.w[4 * w + 2], v.w[4 * w + 3]);
+        }
+    }
+    __device__ __forceinline__ Pack<T, 8> get(int which, int it) const {
+        Pack<T, 8> v;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const uint4 u = at[((which * NSLOT + it) * W + w) * kThreads];
+            v.w[4 * w] = u.x; v.w[4 * w + 1] = u.y; v.w[4 * w + 2] = u.z; v.w[4 * w + 3] = u.w;
+        }
+        return v;
+    }
+    __device__ __forceinline__ void read(int which, int it, float* f) const { unpack<T, 8>(get(which, it), f); }
+    __device__ __forceinline__ T bc(const T* p, long long stride, const SsmArgs& a, long long t0, uint32_t in, int e) const {
+        const int k = e * kThreads + threadIdx.x, row = k / NP, n = k % NP;
+        return row < TT && n < a.N && (in >> (row & 31) & 1) ? p[(t0 + row) * stride + n] : from_f32<T>(0.f);
+    }
+    __device__ __forceinline__ void load(const SsmArgs& a, const ChannelBlock& cb, long long t0, uint32_t in) {
+#pragma unroll
+        for (int it = 0; it < NSLOT; ++it) {
+            const int slot = it * kThreads + threadIdx.x, row = slot / VPR, c0 = (slot % VPR) * 8;
+            const int n = row < TT && (in >> (row & 31) & 1) ? cb.n - c0 : 0;
+            // rows and channels that are not read: any address inside the tensors
+            const long long t = n > 0 ? t0 + row : t0;
+            const int d = n > 0 ? cb.d0 + c0 : cb.d0;
+            load1(0, it, static_cast<const T*>(a.x) + t * a.xs + d, n);
+            load1(1, it, static_cast<const T*>(a.delta) + t * a.ds + d, n);
+            load1(2, it, static_cast<const T*>(a.d_out) + t * a.D + d, n);
+            if (a.z != nullptr) load1(3, it, static_cast<const T*>(a.z) + t * a.zs + d, n);
+        }
+        if constexpr (kAhead) {
+            const T* Bp = static_cast<const T*>(a.Bm) + (long long)cb.g * a.N;
+            const T* Cp = static_cast<const T*>(a.Cm) + (long long)cb.g * a.N;
+#pragma unroll
+            for (int e = 0; e < BPT; ++e) {
+                nB[e] = bc(Bp, a.bs, a, t0, in, e);
+                nC[e] = bc(Cp, a.cs, a, t0, in, e);
             }
         }
+    }
+    // dt, x (or dt x) and dy into shared memory [channel][row], B and C into theirs; zeros in
+    // rows that no sequence covers, which then neither decay nor add anything.
+    template <bool TIMES>
+    __device__ __forceinline__ void lay(const SsmArgs& a, const ChannelBlock& cb, long long t0, uint32_t in, float* s_dt,
+                                        float* s_x, float* s_dy, T* s_B, T* s_C) const {
+        const T* Bp = static_cast<const T*>(a.Bm) + (long long)cb.g * a.N;
+        const T* Cp = static_cast<const T*>(a.Cm) + (long long)cb.g * a.N;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            F2 dt{v[i], v[i + 1]};
-            if (a.delta_bias) dt = add2(dt, F2{i < n ? __ldg(a.delta_bias + d + i) : 0.f, i + 1 < n ? __ldg(a.delta_bias + d + i + 1) : 0.f});
-            if (a.softplus) dt = softplus2(dt);
-            if (i >= n) dt.x = 0.f;
-            if (i + 1 >= n) dt.y = 0.f;
-            const F2 xx = TIMES ? mul2(dt, F2{x[i], x[i + 1]}) : F2{x[i], x[i + 1]};
-            const int o = cell<TT>(c0 + i, row), o2 = cell<TT>(c0 + i + 1, row);
-            s_dt[o] = dt.x;
-            s_dt[o2] = dt.y;
-            s_x[o] = xx.x;
-            s_x[o2] = xx.y;
-            s_dy[o] = g[i];
-            s_dy[o2] = g[i + 1];
+        for (int e = 0; e < BPT; ++e) {
+            const int k = e * kThreads + threadIdx.x;
+            if (k >= TT * NP) continue;
+            s_B[k] = kAhead ? nB[kAhead ? e : 0] : bc(Bp, a.bs, a, t0, in, e);
+            s_C[k] = kAhead ? nC[kAhead ? e : 0] : bc(Cp, a.cs, a, t0, in, e);
+        }
+        cp_async_wait();
+#pragma unroll
+        for (int it = 0; it < NSLOT; ++it) {
+            const int slot = it * kThreads + threadIdx.x, row = slot / VPR, c0 = (slot % VPR) * 8;
+            if (row >= TT) break;
+            const int n = in >> row & 1 ? cb.n - c0 : 0, d = cb.d0 + c0;
+            float xx[8], vv[8], gg[8];
+            read(0, it, xx);
+            read(1, it, vv);
+            read(2, it, gg);
+            if (a.z != nullptr) {
+                float zz[8];
+                read(3, it, zz);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const F2 q{zz[i], zz[i + 1]}, o = mul2(F2{gg[i], gg[i + 1]}, mul2(q, sigmoid2(q)));
+                    gg[i] = o.x;
+                    gg[i + 1] = o.y;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+                F2 dt{vv[i], vv[i + 1]};
+                if (a.delta_bias)
+                    dt = add2(dt, F2{i < n ? __ldg(a.delta_bias + d + i) : 0.f, i + 1 < n ? __ldg(a.delta_bias + d + i + 1) : 0.f});
+                if (a.softplus) dt = softplus2(dt);
+                if (i >= n) dt.x = 0.f;
+                if (i + 1 >= n) dt.y = 0.f;
+                const F2 ox = TIMES ? mul2(dt, F2{xx[i], xx[i + 1]}) : F2{xx[i], xx[i + 1]};
+                const int o = cell<TT>(c0 + i, row), o2 = cell<TT>(c0 + i + 1, row);
+                s_dt[o] = dt.x;
+                s_dt[o2] = dt.y;
+                s_x[o] = ox.x;
+                s_x[o2] = ox.y;
+                s_dy[o] = gg[i];
+                s_dy[o2] = gg[i + 1];
+            }
         }
     }
-}
-
-template <typename T, int TT, int NP>
-__device__ __forceinline__ void stage_bc(const SsmArgs& a, int g, long long t0, uint32_t in, T* s_B, T* s_C) {
-    const T* Bp = static_cast<const T*>(a.Bm) + (long long)g * a.N;
-    const T* Cp = static_cast<const T*>(a.Cm) + (long long)g * a.N;
-#pragma unroll 4
-    for (int k = threadIdx.x; k < TT * NP; k += kThreads) {
-        const int row = k / NP, n = k % NP;
-        const bool on = n < a.N && (in >> row & 1);
-        s_B[k] = on ? Bp[(t0 + row) * a.bs + n] : from_f32<T>(0.f);
-        s_C[k] = on ? Cp[(t0 + row) * a.cs + n] : from_f32<T>(0.f);
-    }
-}
+};
 
 // What the join needs to know of a segment.
 constexpr uint8_t kStarts = 1;      // holds a sequence's first row (its last state is its own)
@@ -205,7 +281,7 @@ struct Place {
 
 template <typename T, int S>
 constexpr size_t summary_smem() {
-    return sizeof(float) * 3 * channels<S>() * tile_rows<S>() + sizeof(T) * 2 * tile_rows<S>() * 4 * S;
+    return Raw<T, S, true>::kBytes + sizeof(float) * 3 * channels<S>() * tile_rows<S>() + sizeof(T) * 2 * tile_rows<S>() * 4 * S;
 }
 
 template <typename T, int S, bool ALIGNED>
@@ -214,7 +290,8 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
                                                                      uint8_t* flags) {
     constexpr int CH = channels<S>(), TT = tile_rows<S>(), NP = 4 * S;
     extern __shared__ __align__(16) float sm[];
-    float *s_dt = sm, *s_u = s_dt + CH * TT, *s_dy = s_u + CH * TT;
+    Raw<T, S, ALIGNED> raw(sm);
+    float *s_dt = sm + Raw<T, S, ALIGNED>::kBytes / 4, *s_u = s_dt + CH * TT, *s_dy = s_u + CH * TT;
     T *s_B = reinterpret_cast<T*>(s_dy + CH * TT), *s_C = s_B + TT * NP;
     const long long sg = blockIdx.x / nblk;
     const ChannelBlock cb = channel_block<CH>(blockIdx.x % nblk, a.D, a.G);
@@ -242,25 +319,40 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
             p[k][m] = F2{1.f, 1.f};
         }
     uint8_t f = 0;
-    for (long long tile = t0; tile < t1; tile += TT) {
-        const Events ev = find_events(a, tile, TT);
+    float* ck[2];   // this thread's checkpoints, and its channels' sums of dt
+    float* dk[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        ck[k] = hck + (t0 / kSub * a.D + at.d[k]) * NP + at.s * 4;
+        dk[k] = dtck + t0 / kSub * a.D + at.d[k];
+    }
+    SeqRange seq{0, 0, 0, false};
+    Events ev = find_events(a, t0, TT, seq), evn{0, 0, 0};
+    raw.load(a, cb, t0, ev.in);
+    for (long long tile = t0; tile < t1; tile += TT, ev = evn) {
         if (tile == t0 && ((ev.first & 1) || !(ev.in & 1))) f |= kFirst;
         if (tile == t0 && !(ev.in & 1)) f |= kEnds;
         if (ev.first) f |= kStarts;
         if (ev.last) f |= kEnds;
         if (tile != t0) __syncthreads();
-        stage<T, CH, TT, ALIGNED, true>(a, cb, tile, ev.in, s_dt, s_u, s_dy);
-        stage_bc<T, TT, NP>(a, cb.g, tile, ev.in, s_B, s_C);
+        raw.template lay<true>(a, cb, tile, ev.in, s_dt, s_u, s_dy, s_B, s_C);
         __syncthreads();
+        if (tile + TT < t1) {
+            evn = find_events(a, tile + TT, TT, seq);
+            raw.load(a, cb, tile + TT, evn.in);
+        }
 #pragma unroll 1
         for (int i0 = 0; i0 < TT; i0 += kSub) {
             if (tile + i0 >= t1) break;
-            const long long r8 = (tile + i0) / kSub;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                for (int m = 0; m < 2; ++m) at.store(hck, r8, a.D, k, m, h[k][m]);
-                if (at.s == 0 && at.live[k]) dtck[r8 * a.D + at.d[k]] = dtsum[k];
+                if (at.live[k]) {
+                    *reinterpret_cast<float2*>(ck[k] + 2 * at.sw) = make_float2(h[k][0].x, h[k][0].y);
+                    *reinterpret_cast<float2*>(ck[k] + 2 - 2 * at.sw) = make_float2(h[k][1].x, h[k][1].y);
+                    if (at.s == 0) *dk[k] = dtsum[k];
+                }
+                ck[k] += (long long)a.D * NP;
+                dk[k] += a.D;
             }
             auto rows = [&](auto evc) {   // eight rows, with or without sequences that begin or end there
                 constexpr bool EV = decltype(evc)::value;
@@ -366,27 +458,23 @@ __global__ void __launch_bounds__(128) ssm_bwd_join_kernel(SsmArgs a, int NP, lo
     }
 }
 
-// The sums over a channel's S lanes of four rows' values v[slot][row], written to
-// the channel's cell of `row` (a multiple of 4): channels are exchanged first (in swapped order), then rows.
-template <int S, int TT>
-__device__ __forceinline__ void lane_sum42(const Place<S>& at, float (&v)[2][4], float* to, int row) {
-    if constexpr (S == 1) {
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<float4*>(to + cell<TT>(at.ch[k], row)) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
-    } else {
+// The sums over a channel's S lanes of four rows' values v[slot][row], in place: channels are
+// exchanged first (in swapped order), then rows.  S = 1: all stay; S = 2: the lane has slot 0's
+// four rows; S >= 4: slot 0's rows 2 (s & 2) / 2 .. + 1 in v[0][0], v[0][1].
+template <int S>
+__device__ __forceinline__ void lane_sum42(const Place<S>& at, float (&v)[2][4]) {
+    if constexpr (S > 1) {
         F2 lo = add2(F2{v[0][0], v[0][1]}, shfl2(F2{v[1][0], v[1][1]}, 1));
         F2 hi = add2(F2{v[0][2], v[0][3]}, shfl2(F2{v[1][2], v[1][3]}, 1));
-        if constexpr (S == 2) {
-            *reinterpret_cast<float4*>(to + cell<TT>(at.ch[0], row)) = make_float4(lo.x, lo.y, hi.x, hi.y);
-        } else {
+        if constexpr (S > 2) {
             const bool up = at.s & 2;   // keeps rows 2 and 3
             F2 keep = up ? hi : lo;
             keep = add2(keep, shfl2(up ? lo : hi, 2));
 #pragma unroll
             for (int m = 4; m < S; m <<= 1) keep = add2(keep, shfl2(keep, m));
-            if (at.s < 4) *reinterpret_cast<float2*>(to + cell<TT>(at.ch[0], row) + (up ? 2 : 0)) = make_float2(keep.x, keep.y);
+            lo = keep;
         }
+        v[0][0] = lo.x; v[0][1] = lo.y; v[0][2] = hi.x; v[0][3] = hi.y;
     }
 }
 
@@ -421,20 +509,13 @@ __device__ __forceinline__ void channel_sum(const Place<S>& at, const F2 (&dB)[2
     }
 }
 
-// Asynchronous copies of a thread's own checkpoint (8 floats, two sums of dt) into its slots
-// of shared memory, one checkpoint ahead of its use.
-__device__ __forceinline__ void cp_async8(float* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async4(float* dst, const float* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// A thread's own checkpoint (8 floats, two sums of dt) in its slots of shared memory, copied one
+// checkpoint ahead of its use.
 constexpr int kCk = 10 * kThreads;   // [4 pairs][thread] of float2, then [2][thread]
 
 template <typename T, int S>
 constexpr size_t grad_smem() {
-    return sizeof(float) * (6 * channels<S>() * tile_rows<S>() + 2 * kWarps * kSub * 2 * 4 * S + 3 * kCk) +
+    return Raw<T, S, true>::kBytes + sizeof(float) * (3 * channels<S>() * tile_rows<S>() + 2 * kWarps * kSub * 2 * 4 * S + 3 * kCk + 8 * kThreads) +
            sizeof(T) * 2 * tile_rows<S>() * 4 * S;
 }
 
@@ -444,10 +525,11 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                                                                   float* part, float* bcpart) {
     constexpr int CH = channels<S>(), TT = tile_rows<S>(), NP = 4 * S, VPR = CH / 8;
     extern __shared__ __align__(16) float sm[];
-    float *s_dt = sm, *s_x = s_dt + CH * TT, *s_dy = s_x + CH * TT;
-    float *s_p = s_dy + CH * TT, *s_q = s_p + CH * TT, *s_y = s_q + CH * TT, *s_red = s_y + CH * TT;
+    Raw<T, S, ALIGNED> raw(sm);
+    // dt, x and dy of the tile; eight rows on, dx, ddelta (without softplus' slope) and y in their place
+    float *s_dt = sm + Raw<T, S, ALIGNED>::kBytes / 4, *s_x = s_dt + CH * TT, *s_dy = s_x + CH * TT, *s_red = s_dy + CH * TT;
     float* s_ck = s_red + 2 * kWarps * kSub * 2 * NP;   // two checkpoints, then the segment's incoming state
-    T *s_B = reinterpret_cast<T*>(s_ck + 3 * kCk), *s_C = s_B + TT * NP;
+    T *s_B = reinterpret_cast<T*>(s_ck + 3 * kCk + 8 * kThreads), *s_C = s_B + TT * NP;
     const long long sg = blockIdx.x / nblk;
     const int blk = blockIdx.x % nblk, tid = threadIdx.x;
     const ChannelBlock cb = channel_block<CH>(blk, a.D, a.G);
@@ -468,14 +550,23 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
         }
     auto slot = [&](int which, int k, int m) { return s_ck + which * kCk + ((k * 2 + m) * kThreads + tid) * 2; };
     auto slot_dt = [&](int which, int k) { return s_ck + which * kCk + 8 * kThreads + k * kThreads + tid; };
-    auto fetch = [&](long long row, int which) {   // the checkpoint in front of `row`
-        const long long r8 = row / kSub;
+    const float* ck[2];   // the checkpoint that is fetched next
+    const float* dk[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        ck[k] = hck + ((t1 - 1) / kSub * a.D + at.d[k]) * NP + at.s * 4;
+        dk[k] = dtck + (t1 - 1) / kSub * a.D + at.d[k];
+    }
+    auto fetch = [&](int which) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            if (!at.live[k]) continue;
-#pragma unroll
-            for (int m = 0; m < 2; ++m) cp_async8(slot(which, k, m), hck + (r8 * a.D + at.d[k]) * NP + at.n(m));
-            cp_async4(slot_dt(which, k), dtck + r8 * a.D + at.d[k]);
+            if (at.live[k]) {
+                cp_async8(slot(which, k, 0), ck[k] + 2 * at.sw);
+                cp_async8(slot(which, k, 1), ck[k] + 2 - 2 * at.sw);
+                cp_async4(slot_dt(which, k), dk[k]);
+            }
+            ck[k] -= (long long)a.D * NP;
+            dk[k] -= a.D;
         }
     };
 #pragma unroll
@@ -490,32 +581,47 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                     *slot_dt(w, k) = 0.f;
                 }
         }
-    fetch((t1 - 1) / kSub * kSub, 0);
-    float sD[8] = {}, sb[8] = {};
+    fetch(0);
+    F2 sD[S == 1 ? 2 : 1] = {};     // dy x of the rows that this lane finishes
+    float skip[2];
+    float* s_sb = s_ck + 3 * kCk + tid;   // this thread's sums of ddelta over its rows, [8][thread]
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_sb[i * kThreads] = 0.f;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) skip[k] = a.Dskip && at.live[k] ? a.Dskip[at.d[k]] : 0.f;
     int phase = 0;
 
-    for (long long tile = t0 + (t1 - t0 - 1) / TT * TT; tile >= t0; tile -= TT) {
-        const Events ev = find_events(a, tile, TT);
-        stage<T, CH, TT, ALIGNED, false>(a, cb, tile, ev.in, s_dt, s_x, s_dy);
-        stage_bc<T, TT, NP>(a, cb.g, tile, ev.in, s_B, s_C);
+    const long long last_tile = t0 + (t1 - t0 - 1) / TT * TT;
+    SeqRange seq = r0;
+    Events ev = find_events(a, last_tile, TT, seq), evn{0, 0, 0};
+    raw.load(a, cb, last_tile, ev.in);
+    float* bc = bcpart + ((long long)blk * a.M + last_tile) * 2 * a.N;   // the tile's dB, dC of this channel block
+    for (long long tile = last_tile; tile >= t0; tile -= TT, ev = evn, bc -= 2 * TT * (long long)a.N) {
+        raw.template lay<false>(a, cb, tile, ev.in, s_dt, s_x, s_dy, s_B, s_C);
         __syncthreads();
 #pragma unroll 1
         for (int i0 = TT - kSub; i0 >= 0; i0 -= kSub) {
             if (tile + i0 >= t1) continue;
-            F2 hs[2][2];   // the state in front of these rows
+            // the state in front of these rows: the checkpoint, and what reaches it of the segment's
             cp_async_wait();
+            if (tile + i0 < reach) {
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+                for (int k = 0; k < 2; ++k) {
+                    const F2 cum = both(*slot_dt(phase, k));
 #pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                    const float2 v = *reinterpret_cast<const float2*>(slot(phase, k, m));
-                    hs[k][m] = F2{v.x, v.y};
-                    if (tile + i0 < reach) {
+                    for (int m = 0; m < 2; ++m) {
+                        float2* v = reinterpret_cast<float2*>(slot(phase, k, m));
                         const float2 in = *reinterpret_cast<const float2*>(slot(2, k, m));
-                        hs[k][m] = fma2(ex2(mul2(both(*slot_dt(phase, k)), A2[k][m])), F2{in.x, in.y}, hs[k][m]);
+                        const F2 o = fma2(ex2(mul2(cum, A2[k][m])), F2{in.x, in.y}, F2{v->x, v->y});
+                        *v = make_float2(o.x, o.y);
                     }
                 }
-            if (tile + i0 > t0) fetch(tile + i0 - kSub, phase ^ 1);
+            }
+            auto in_front = [&](int k, int m) {
+                const float2 v = *reinterpret_cast<const float2*>(slot(phase, k, m));
+                return F2{v.x, v.y};
+            };
+            if (tile + i0 > t0) fetch(phase ^ 1);
             float* red = s_red + (phase * kWarps + at.warp) * kSub * 2 * NP;
             auto rows = [&](auto evc) {
                 constexpr bool EV = decltype(evc)::value;
@@ -541,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                             for (int k = 0; k < 2; ++k) {
                                 const float dt = j == 0 ? d4[k].x : j == 1 ? d4[k].y : j == 2 ? d4[k].z : d4[k].w;
                                 const float x = j == 0 ? x4[k].x : j == 1 ? x4[k].y : j == 2 ? x4[k].z : x4[k].w;
-                                F2 hp = r > 0 ? ha[r > 0 ? r - 1 : 0][k][m] : hs[k][m];
+                                F2 hp = r > 0 ? ha[r > 0 ? r - 1 : 0][k][m] : in_front(k, m);
                                 if (first) hp = at.get(a.h0, sr.q, a, k, m);
                                 ea[r][k][m] = ex2(mul2(both(dt), A2[k][m]));
                                 ha[r][k][m] = fma2(ea[r][k][m], hp, mul2(both(dt * x), B));
@@ -580,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                             F2 p{0.f, 0.f}, q{0.f, 0.f}, y{0.f, 0.f};
 #pragma unroll
                             for (int m = 0; m < 2; ++m) {
-                                F2 hp = r > 0 ? ha[r > 0 ? r - 1 : 0][k][m] : hs[k][m];
+                                F2 hp = r > 0 ? ha[r > 0 ? r - 1 : 0][k][m] : in_front(k, m);
                                 if (first) hp = at.get(a.h0, sr.q, a, k, m);
                                 if (last) dh[k][m] = at.get(a.d_hT, sr.q, a, k, m);
                                 dh[k][m] = fma2(C[m], both(dy), dh[k][m]);
@@ -603,9 +709,32 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                         }
                         channel_sum<S>(at, dB, dC, red + r * 2 * NP);
                     }
-                    lane_sum42<S, TT>(at, pv, s_p, i0 + i);
-                    lane_sum42<S, TT>(at, qv, s_q, i0 + i);
-                    lane_sum42<S, TT>(at, yv, s_y, i0 + i);
+                    // p, q and y over the lanes; the lane that ends with a row (or two, or four) of a
+                    // channel finishes it, in place of the row's dt, x and dy, which all lanes have read
+                    lane_sum42<S>(at, pv);
+                    lane_sum42<S>(at, qv);
+                    lane_sum42<S>(at, yv);
+#pragma unroll
+                    for (int k = 0; k < (S == 1 ? 2 : 1); ++k) {
+#pragma unroll
+                        for (int w = 0; w < (S >= 4 ? 1 : 2); ++w) {
+                            const bool up = S >= 4 ? (at.s & 2) != 0 : w;
+                            const F2 dt = up ? F2{d4[k].z, d4[k].w} : F2{d4[k].x, d4[k].y};
+                            const F2 x = up ? F2{x4[k].z, x4[k].w} : F2{x4[k].x, x4[k].y};
+                            const F2 dy = up ? F2{g4[k].z, g4[k].w} : F2{g4[k].x, g4[k].y};
+                            const F2 p{pv[k][2 * w], pv[k][2 * w + 1]}, q{qv[k][2 * w], qv[k][2 * w + 1]}, y{yv[k][2 * w], yv[k][2 * w + 1]};
+                            const F2 ox = fma2(p, dt, mul2(both(skip[k]), dy));
+                            const F2 ov = fma2(p, x, mul2(q, both(1.0f / kLog2e)));
+                            const F2 oy = fma2(both(skip[k]), x, y);
+                            sD[k] = fma2(dy, x, sD[k]);
+                            if (S < 8 || at.s < 4) {
+                                const int o = cell<TT>(at.ch[k], i0 + i) + (up ? 2 : 0);
+                                *reinterpret_cast<float2*>(s_dt + o) = make_float2(ox.x, ox.y);
+                                *reinterpret_cast<float2*>(s_x + o) = make_float2(ov.x, ov.y);
+                                *reinterpret_cast<float2*>(s_dy + o) = make_float2(oy.x, oy.y);
+                            }
+                        }
+                    }
                 }
             };
             if ((ev.first | ev.last) >> i0 & ((1u << kSub) - 1)) rows(std::true_type{});
@@ -617,52 +746,58 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                 float t = 0.f;
 #pragma unroll
                 for (int x = 0; x < kWarps; ++x) t += s_red[(phase * kWarps + x) * kSub * 2 * NP + k];
-                bcpart[(((long long)blk * a.M + tile + i0 + r) * 2 + w) * a.N + n] = t;
+                bc[((i0 + r) * 2 + w) * a.N + n] = t;
             }
             phase ^= 1;
         }
-        // rows and channels as they were staged: dx, ddelta, dz; dDskip and the bias' gradient
-        // (every lane's p, q and y were written before the last barrier)
-#pragma unroll 1
-        for (int slot = tid; slot < TT * VPR; slot += kThreads) {
-            const int row = slot / VPR, c0 = (slot % VPR) * 8;
+        // rows and channels as they were staged: dx, ddelta, dz and the bias' gradient (what the
+        // lanes left was written before the last barrier).  The raw inputs are read once more,
+        // and the next tile's take their place while these are worked on.
+        constexpr int NSLOT = Raw<T, S, ALIGNED>::NSLOT;
+        Pack<T, 8> pv[NSLOT], pg[NSLOT], pz[NSLOT];
+#pragma unroll
+        for (int it = 0; it < NSLOT; ++it) {
+            pv[it] = raw.get(1, it);
+            pg[it] = raw.get(2, it);
+            pz[it] = raw.get(3, it);   // without a z: nothing that is used
+        }
+        if (tile > t0) {
+            evn = find_events(a, tile - TT, TT, seq);
+            raw.load(a, cb, tile - TT, evn.in);
+        }
+#pragma unroll
+        for (int it = 0; it < NSLOT; ++it) {
+            const int slot = it * kThreads + tid, row = slot / VPR, c0 = (slot % VPR) * 8;
             const int cn = max(0, min(8, cb.n - c0)), d = cb.d0 + c0;
-            if (!(ev.in >> row & 1) || cn == 0) continue;
+            if (row >= TT || !(ev.in >> row & 1) || cn == 0) continue;
             const long long t = tile + row;
-            float v[8], dx[8], z[8], g[8];
-            unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.delta) + t * a.ds + d, cn), v);
-            if (a.z != nullptr) {
-                unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.z) + t * a.zs + d, cn), z);
-                unpack<T, 8>(load8<T, ALIGNED>(static_cast<const T*>(a.d_out) + t * a.D + d, cn), g);
-            }
+            float dx[8], v[8], z[8], g[8];
+            unpack<T, 8>(pv[it], v);
+            unpack<T, 8>(pg[it], g);
+            unpack<T, 8>(pz[it], z);
 #pragma unroll
             for (int i = 0; i < 8; i += 2) {
                 const int o = cell<TT>(c0 + i, row), o2 = cell<TT>(c0 + i + 1, row);
-                const F2 dt{s_dt[o], s_dt[o2]}, x{s_x[o], s_x[o2]}, dy{s_dy[o], s_dy[o2]}, p{s_p[o], s_p[o2]};
-                F2 sk{0.f, 0.f};
-                if (a.Dskip) sk = F2{i < cn ? __ldg(a.Dskip + d + i) : 0.f, i + 1 < cn ? __ldg(a.Dskip + d + i + 1) : 0.f};
-                const F2 ox = fma2(p, dt, mul2(sk, dy));
-                F2 ov = fma2(p, x, mul2(F2{s_q[o], s_q[o2]}, both(1.0f / kLog2e)));
+                dx[i] = s_dt[o];
+                dx[i + 1] = s_dt[o2];
+                F2 ov{s_x[o], s_x[o2]};
                 if (a.softplus) {
-                    F2 raw{v[i], v[i + 1]};
-                    if (a.delta_bias) raw = add2(raw, F2{i < cn ? __ldg(a.delta_bias + d + i) : 0.f, i + 1 < cn ? __ldg(a.delta_bias + d + i + 1) : 0.f});
-                    ov = mul2(ov, sigmoid2(raw));
+                    F2 dl{v[i], v[i + 1]};
+                    if (a.delta_bias)
+                        dl = add2(dl, F2{i < cn ? __ldg(a.delta_bias + d + i) : 0.f, i + 1 < cn ? __ldg(a.delta_bias + d + i + 1) : 0.f});
+                    ov = mul2(ov, sigmoid2(dl));
                 }
+                s_sb[i * kThreads] += ov.x;
+                s_sb[(i + 1) * kThreads] += ov.y;
+                v[i] = ov.x;
+                v[i + 1] = ov.y;
                 if (a.z != nullptr) {
-                    const F2 zz{z[i], z[i + 1]}, sg1 = sigmoid2(zz), y = fma2(sk, x, F2{s_y[o], s_y[o2]});
+                    const F2 zz{z[i], z[i + 1]}, sg1 = sigmoid2(zz);
                     const F2 slope = mul2(sg1, fma2(zz, fma2(sg1, both(-1.0f), both(1.0f)), both(1.0f)));
-                    const F2 oz = mul2(mul2(F2{g[i], g[i + 1]}, y), slope);
+                    const F2 oz = mul2(mul2(F2{g[i], g[i + 1]}, F2{s_dy[o], s_dy[o2]}), slope);
                     z[i] = oz.x;
                     z[i + 1] = oz.y;
                 }
-                sD[i] = fmaf(dy.x, x.x, sD[i]);
-                sD[i + 1] = fmaf(dy.y, x.y, sD[i + 1]);
-                sb[i] += ov.x;
-                sb[i + 1] += ov.y;
-                dx[i] = ox.x;
-                dx[i + 1] = ox.y;
-                v[i] = ov.x;
-                v[i + 1] = ov.y;
             }
             store8<T, ALIGNED>(static_cast<T*>(a.dx) + t * a.D + d, dx, cn);
             store8<T, ALIGNED>(static_cast<T*>(a.ddelta) + t * a.D + d, v, cn);
@@ -676,22 +811,22 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int m = 0; m < 2; ++m) at.put(pseg, 0, a, k, m, dA[k][m]);
-    // over the rows: a thread's slots all have the same channels; RPP partial sums per channel
-    constexpr int RPP = kThreads / VPR > 0 ? kThreads / VPR : 1;
-    float* s0 = sm;   // [2][RPP][CH]
-    static_assert(VPR <= kThreads && sizeof(float) * 2 * RPP * CH <= grad_smem<T, S>(), "shared memory holds the partial sums");
+    // dDskip: over the two (S >= 4) lanes that finish a channel's rows
+    float* pD = pseg + (long long)a.D * a.N;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        s0[(tid / VPR) * CH + (tid % VPR) * 8 + i] = sD[i];
-        s0[(RPP + tid / VPR) * CH + (tid % VPR) * 8 + i] = sb[i];
+    for (int k = 0; k < (S == 1 ? 2 : 1); ++k) {
+        float t = sD[k].x + sD[k].y;
+        if (S >= 4) t += __shfl_xor_sync(0xffffffffu, t, 2);
+        if (at.live[k] && at.s < 2) pD[at.d[k]] = t;
     }
+    // the bias: a thread's slots all have the same channels; RPP partial sums per channel
+    constexpr int RPP = kThreads / VPR;
+    const float* s0 = s_ck + 3 * kCk;
     __syncthreads();
-    for (int k = tid; k < 2 * CH; k += kThreads) {
-        const int w = k / CH, c = k % CH;
-        if (c >= cb.n) continue;
+    for (int c = tid; c < cb.n; c += kThreads) {
         float t = 0.f;
-        for (int r = 0; r < RPP; ++r) t += s0[(w * RPP + r) * CH + c];
-        pseg[(long long)a.D * a.N + (long long)w * a.D + cb.d0 + c] = t;
+        for (int r = 0; r < RPP; ++r) t += s0[(c % 8) * kThreads + r * VPR + c / 8];
+        pD[a.D + cb.d0 + c] = t;
     }
 }
 
