@@ -165,14 +165,20 @@ def _workspace(ws, nbytes, device):
     return (None, None, 0) if ws is None else (ws, ws.data_ptr(), ws.numel() * ws.element_size())
 
 
+_NULL = contextlib.nullcontext()
+# The current stream's handle without building a torch.cuda.Stream object (a microsecond of the
+# few that a small call takes on the host).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _on(device):
     """The device of the tensors as the current one, for the launch."""
-    if device.index is None or torch.cuda.current_device() == device.index:
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _NULL if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _stream(device):
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -225,12 +225,101 @@ __device__ __forceinline__ void store_f32(T* p, const float* f) {
     store_pack<T, VEC>(p, pack<T, VEC>(f));
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float ex2(float v) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Two fp32 values in a register pair; one instruction works on both (the same roundings as
+// two scalar ones, half the issue slots).
+struct F2 {
+    float x, y;
+};
+__device__ __forceinline__ unsigned long long f2_bits(F2 a) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+    return r;
+}
+__device__ __forceinline__ F2 f2_of(unsigned long long v) {
+    F2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return f2_of(r);
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+    return f2_of(r);
+}
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+    return f2_of(r);
+}
+__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
+__device__ __forceinline__ F2 ex2(F2 v) { return F2{ex2(v.x), ex2(v.y)}; }
+__device__ __forceinline__ F2 rcp(F2 v) {
+    F2 r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
+    return r;
+}
+
+// The functions of the step size and the gate work on pairs and take the hardware's exponential
+// and reciprocal: each within a few units, |v| log2(e) more through the exponent's rounding.
+__device__ __forceinline__ F2 sigmoid2(F2 v) { return rcp(add2(both(1.0f), ex2(mul2(v, both(-kLog2e))))); }
+
+// a * b + c, a + b and a * b over VEC values, in pairs where there are pairs.
+template <int VEC>
+__device__ __forceinline__ void fma_n(const float* a, const float* b, float* c) {   // c += a * b
+    if constexpr (VEC == 1) {
+        c[0] = fmaf(a[0], b[0], c[0]);
+    } else {
+#pragma unroll
+        for (int v = 0; v < VEC; v += 2) {
+            const F2 o = fma2(F2{a[v], a[v + 1]}, F2{b[v], b[v + 1]}, F2{c[v], c[v + 1]});
+            c[v] = o.x;
+            c[v + 1] = o.y;
+        }
+    }
+}
+
 // 1 / (1 + e^-v).  FAST (bf16 outputs): the hardware exponential and quotient, within a few
 // fp32 units, far below the output's rounding; otherwise the full-precision functions.
 template <bool FAST>
 __device__ __forceinline__ float sigmoid(float v) {
     if constexpr (FAST) return __fdividef(1.0f, 1.0f + __expf(-v));
     return 1.0f / (1.0f + expf(-v));
+}
+
+// v sigmoid(v) and its derivative sigmoid(v) (1 + v (1 - sigmoid(v))) over VEC values.
+template <int VEC, bool FAST>
+__device__ __forceinline__ void sigmoid_n(const float* v, float* s) {
+    if constexpr (FAST && VEC > 1) {
+#pragma unroll
+        for (int i = 0; i < VEC; i += 2) {
+            const F2 o = sigmoid2(F2{v[i], v[i + 1]});
+            s[i] = o.x;
+            s[i + 1] = o.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) s[i] = sigmoid<FAST>(v[i]);
+    }
+}
+template <int VEC, bool FAST>
+__device__ __forceinline__ void silu_n(float* v) {
+    float s[VEC];
+    sigmoid_n<VEC, FAST>(v, s);
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) v[i] *= s[i];
 }
 
 // Whether every access of VEC * el bytes at p + k * stride_bytes is aligned.

@@ -43,34 +43,40 @@ __device__ __forceinline__ void load_taps(const float* w, const float* bias, int
 // Inputs t - (WM-1) .. t - 1 of the sequence r (from its state in front of row r.b).
 template <typename T, int VEC, int WM>
 __device__ __forceinline__ void load_window(const ConvArgs& a, const SeqRange& r, long long t, long long d0,
-                                            Pack<T, VEC>* win) {
+                                            float (*win)[VEC]) {
     const T* x = static_cast<const T*>(a.x) + d0;
     const T* st = static_cast<const T*>(a.state0);
 #pragma unroll
     for (int j = 0; j < WM - 1; ++j) {
         const long long p = t - (WM - 1) + j;
-        win[j] = zero_pack<T, VEC>();
+        Pack<T, VEC> row = zero_pack<T, VEC>();
         if (p >= r.b) {
-            win[j] = load_pack<VEC>(x + p * a.xs);
+            row = load_pack<VEC>(x + p * a.xs);
         } else if (st != nullptr) {
             const int k = a.W - 1 + (int)(p - r.b);
-            if (k >= 0) win[j] = load_pack<VEC>(st + ((long long)r.q * (a.W - 1) + k) * a.D + d0);
+            if (k >= 0) row = load_pack<VEC>(st + ((long long)r.q * (a.W - 1) + k) * a.D + d0);
         }
+        unpack<T, VEC>(row, win[j]);
     }
 }
 
-template <typename T, int VEC, int WM>
-__device__ __forceinline__ void conv_pre(const Pack<T, VEC>* win, const Pack<T, VEC>& cur, const float (*wr)[VEC],
-                                         const float* br, float* pre) {
+// The W rows in front of and at row t, in fp32 (unpacked once when a row enters).
+template <int VEC, int WM>
+__device__ __forceinline__ void conv_pre(const float (*win)[VEC], const float* cur, const float (*wr)[VEC], const float* br,
+                                         float* pre) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) pre[v] = br[v];
 #pragma unroll
-    for (int j = 0; j < WM; ++j) {
-        float f[VEC];
-        unpack<T, VEC>(j < WM - 1 ? win[j < WM - 1 ? j : 0] : cur, f);
+    for (int j = 0; j < WM; ++j) fma_n<VEC>(wr[j], j < WM - 1 ? win[j < WM - 1 ? j : 0] : cur, pre);
+}
+template <int VEC, int WM>
+__device__ __forceinline__ void shift_in(float (*win)[VEC], const float* cur) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) pre[v] = fmaf(wr[j][v], f[v], pre[v]);
-    }
+    for (int j = 0; j + 1 < WM - 1; ++j)
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) win[j][v] = win[j + 1][v];
+#pragma unroll
+    for (int v = 0; v < VEC; ++v) win[WM - 2][v] = cur[v];
 }
 
 template <typename T, int VEC, int WM, bool SILU>
@@ -99,34 +105,39 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int run, long
     float wr[WM][VEC], br[VEC];
     load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
     T* out = static_cast<T*>(a.out) + d0;
-    Pack<T, VEC> win[WM - 1];
+    float win[WM - 1][VEC];
 
     long long t = who * run;
     const long long t1 = t + run < a.M ? t + run : a.M;
-    auto emit = [&](long long row, const Pack<T, VEC>& cur) {
-        float pre[VEC];
-        conv_pre<T, VEC, WM>(win, cur, wr, br, pre);
-        if (SILU) {
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) pre[v] *= sigmoid<kFast>(pre[v]);
-        }
+    auto emit = [&](long long row, const Pack<T, VEC>& raw) {
+        float cur[VEC], pre[VEC];
+        unpack<T, VEC>(raw, cur);
+        conv_pre<VEC, WM>(win, cur, wr, br, pre);
+        if (SILU) silu_n<VEC, kFast>(pre);
         store_f32<T, VEC>(out + row * a.D, pre);
-#pragma unroll
-        for (int j = 0; j + 1 < WM - 1; ++j) win[j] = win[j + 1];
-        win[WM - 2] = cur;
+        shift_in<VEC, WM>(win, cur);
     };
     while (t < t1) {
         const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, t);
         if (!r.ok) { ++t; continue; }
         const long long stop = t1 < r.e ? t1 : r.e;
         load_window<T, VEC, WM>(a, r, t, d0, win);
-        constexpr int U = 4;
-        for (; t + U <= stop; t += U) {
-            Pack<T, VEC> nx[U];
+        constexpr int U = 4;   // rows in flight: the next four are loaded before these are worked on
+        Pack<T, VEC> nx[U];
+        if (t + U <= stop) {
 #pragma unroll
             for (int u = 0; u < U; ++u) nx[u] = load_pack<VEC>(x + (t + u) * a.xs);
+        }
+        for (; t + U <= stop; t += U) {
+            Pack<T, VEC> cur[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) emit(t + u, nx[u]);
+            for (int u = 0; u < U; ++u) cur[u] = nx[u];
+            if (t + 2 * U <= stop) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) nx[u] = load_pack<VEC>(x + (t + U + u) * a.xs);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) emit(t + u, cur[u]);
         }
         for (; t < stop; ++t) emit(t, load_pack<VEC>(x + t * a.xs));
     }
@@ -147,13 +158,13 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
         if (k >= 0) win[j] = load_pack<VEC>(st + (long long)k * a.D);
     }
     const Pack<T, VEC> cur = load_pack<VEC>(static_cast<const T*>(a.x) + n * a.xs + d0);
-    float wr[WM][VEC], br[VEC], pre[VEC];
+    float wr[WM][VEC], br[VEC], pre[VEC], fw[WM - 1][VEC], fc[VEC];
     load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
-    conv_pre<T, VEC, WM>(win, cur, wr, br, pre);
-    if (SILU) {
 #pragma unroll
-        for (int v = 0; v < VEC; ++v) pre[v] *= sigmoid<sizeof(T) == 2>(pre[v]);
-    }
+    for (int j = 0; j < WM - 1; ++j) unpack<T, VEC>(win[j], fw[j]);
+    unpack<T, VEC>(cur, fc);
+    conv_pre<VEC, WM>(fw, fc, wr, br, pre);
+    if (SILU) silu_n<VEC, sizeof(T) == 2>(pre);
     store_f32<T, VEC>(static_cast<T*>(a.out) + n * a.D + d0, pre);
 #pragma unroll
     for (int j = 1; j < WM - 1; ++j) {
@@ -191,7 +202,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
                 const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, p0);
                 if (!r.ok) { ++p0; continue; }
                 const long long p1 = rend < r.e ? rend : r.e;
-                Pack<T, VEC> win[WM - 1];
+                float win[WM - 1][VEC];
                 load_window<T, VEC, WM>(a, r, p0, d0, win);
                 float dp[WM][VEC] = {};   // dp[j] = dpre[t - j]
                 // row t enters; row s = t - (WM-1) has all of its gradients and leaves
@@ -207,21 +218,19 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
                     if (dfin != nullptr && k >= 0)
                         unpack<T, VEC>(load_pack<VEC>(dfin + ((long long)r.q * (a.W - 1) + k) * a.D + d0), g);
 #pragma unroll
-                    for (int j = 0; j < WM; ++j)
-#pragma unroll
-                        for (int v = 0; v < VEC; ++v) g[v] = fmaf(wr[j][v], dp[j][v], g[v]);
+                    for (int j = 0; j < WM; ++j) fma_n<VEC>(wr[j], dp[j], g);
                     store_f32<T, VEC>(to, g);
                 };
                 auto enter = [&](const Pack<T, VEC>& cur, const Pack<TG, VEC>& gcur, bool mine) {
-                    float pre[VEC], g[VEC];
+                    float cf[VEC], g[VEC];
+                    unpack<T, VEC>(cur, cf);
                     unpack<TG, VEC>(gcur, g);
                     if (SILU) {
-                        conv_pre<T, VEC, WM>(win, cur, wr, br, pre);
+                        float pre[VEC], sg[VEC];
+                        conv_pre<VEC, WM>(win, cf, wr, br, pre);
+                        sigmoid_n<VEC, kFast>(pre, sg);
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v) {
-                            const float sg = sigmoid<kFast>(pre[v]);
-                            g[v] *= sg * fmaf(pre[v], 1.0f - sg, 1.0f);
-                        }
+                        for (int v = 0; v < VEC; ++v) g[v] *= sg[v] * fmaf(pre[v], 1.0f - sg[v], 1.0f);
                     }
 #pragma unroll
                     for (int j = WM - 1; j > 0; --j)
@@ -233,30 +242,34 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) db[v] += g[v];
 #pragma unroll
-                        for (int j = 0; j < WM; ++j) {
-                            float f[VEC];
-                            unpack<T, VEC>(j < WM - 1 ? win[j < WM - 1 ? j : 0] : cur, f);
-#pragma unroll
-                            for (int v = 0; v < VEC; ++v) dw[j][v] = fmaf(g[v], f[v], dw[j][v]);
-                        }
+                        for (int j = 0; j < WM; ++j) fma_n<VEC>(g, j < WM - 1 ? win[j < WM - 1 ? j : 0] : cf, dw[j]);
                     }
-#pragma unroll
-                    for (int j = 0; j + 1 < WM - 1; ++j) win[j] = win[j + 1];
-                    win[WM - 2] = cur;
+                    shift_in<VEC, WM>(win, cf);
                 };
                 long long t = p0;
-                constexpr int U = 4;
-                for (; t + U <= p1; t += U) {
-                    Pack<T, VEC> nx[U];
-                    Pack<TG, VEC> ng[U];
+                constexpr int U = 4;   // the next four rows are loaded before these are worked on
+                Pack<T, VEC> nx[U];
+                Pack<TG, VEC> ng[U];
+                auto fetch = [&](long long at) {
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        nx[u] = load_pack<VEC>(x + (t + u) * a.xs);
-                        ng[u] = load_pack<VEC>(dy + (t + u) * a.D);
+                        nx[u] = load_pack<VEC>(x + (at + u) * a.xs);
+                        ng[u] = load_pack<VEC>(dy + (at + u) * a.D);
                     }
+                };
+                if (t + U <= p1) fetch(t);
+                for (; t + U <= p1; t += U) {
+                    Pack<T, VEC> cx[U];
+                    Pack<TG, VEC> cg[U];
 #pragma unroll
                     for (int u = 0; u < U; ++u) {
-                        enter(nx[u], ng[u], true);
+                        cx[u] = nx[u];
+                        cg[u] = ng[u];
+                    }
+                    if (t + 2 * U <= p1) fetch(t + U);
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        enter(cx[u], cg[u], true);
                         leave(t + u);
                     }
                 }
@@ -400,9 +413,11 @@ bool rows_ok(const ConvArgs& a, int el, int vec) {
            vec_ok(a.d_stateT, row, by);
 }
 
+// The forward takes four channels per thread in either type: with eight, the window, the taps
+// and the rows in flight need 128 registers, and too few warps remain to cover the loads.
 template <typename T>
 cudaError_t fwd_t(const ConvArgs& a, bool silu, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 4;
     if (rows_ok(a, sizeof(T), V)) return silu ? fwd_w<T, V, true>(a, s) : fwd_w<T, V, false>(a, s);
     return silu ? fwd_w<T, 1, true>(a, s) : fwd_w<T, 1, false>(a, s);
 }

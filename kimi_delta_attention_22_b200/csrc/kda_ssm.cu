@@ -318,76 +318,116 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a, Segments seg, 
 }
 
 // One row of every sequence: the fp32 state is read and written once, which bounds the step.
-// S lanes per channel, four states per lane (one 16-byte access where N is a multiple of 4);
-// a thread takes the same channel of up to four sequences, their loads first.
-template <typename T, int S, bool VEC4>
+// S lanes per channel, NQ runs of four states per lane (one 16-byte access each where N is a
+// multiple of 4); a thread takes the same channel of two sequences, all of their loads first.
+template <typename T, int S, int NQ, bool VEC4>
 __global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
-    constexpr int NB = 4;
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    constexpr int NB = 2;
+    const unsigned i = blockIdx.x * 256u + threadIdx.x;
     const int s = (int)(i % S);
-    const bool live = i / S < a.D;
+    const bool live = i / S < (unsigned)a.D;
     const int d = live ? (int)(i / S) : 0;
-    const int n0 = s * 4, g = d / (a.D / a.G);
+    const int g = a.G == 1 ? 0 : d / (a.D / a.G);
     const long long q0 = (long long)blockIdx.y * NB;
-    float A2[4], h[NB][4], B[NB][4], C[NB][4], x[NB], v[NB], z[NB];
+    float h[NB][NQ * 4], x[NB], v[NB], z[NB];
+    Pack<T, 4> B[NB][NQ], C[NB][NQ];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const long long q = q0 + b;
         const bool on = live && q < a.num_seqs;
+        const float* hp = a.hT + (q * a.D + d) * a.N;
+        const T* Bp = static_cast<const T*>(a.Bm) + q * a.bs + (long long)g * a.N;
+        const T* Cp = static_cast<const T*>(a.Cm) + q * a.cs + (long long)g * a.N;
+#pragma unroll
+        for (int k = 0; k < NQ; ++k) {
+            const int n0 = (k * S + s) * 4;
+            B[b][k] = C[b][k] = zero_pack<T, 4>();
+            if (VEC4) {
+                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (on && n0 < a.N) {
+                    f = *reinterpret_cast<const float4*>(hp + n0);
+                    B[b][k] = load_pack<4>(Bp + n0);
+                    C[b][k] = load_pack<4>(Cp + n0);
+                }
+                h[b][4 * k] = f.x; h[b][4 * k + 1] = f.y; h[b][4 * k + 2] = f.z; h[b][4 * k + 3] = f.w;
+            } else {
+                float fb[4], fc[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const bool in = on && n0 + j < a.N;
+                    h[b][4 * k + j] = in ? hp[n0 + j] : 0.f;
+                    fb[j] = in ? to_f32<T>(Bp[n0 + j]) : 0.f;
+                    fc[j] = in ? to_f32<T>(Cp[n0 + j]) : 0.f;
+                }
+                B[b][k] = pack<T, 4>(fb);   // exact: they were of this type
+                C[b][k] = pack<T, 4>(fc);
+            }
+        }
         x[b] = on ? to_f32<T>(static_cast<const T*>(a.x)[q * a.xs + d]) : 0.f;
         v[b] = on ? to_f32<T>(static_cast<const T*>(a.delta)[q * a.ds + d]) : 0.f;
         z[b] = on && a.z ? to_f32<T>(static_cast<const T*>(a.z)[q * a.zs + d]) : 0.f;
-        const float* hp = a.hT + (q * a.D + d) * a.N + n0;
-        const T* Bp = static_cast<const T*>(a.Bm) + q * a.bs + (long long)g * a.N + n0;
-        const T* Cp = static_cast<const T*>(a.Cm) + q * a.cs + (long long)g * a.N + n0;
+    }
+    float A2[NQ * 4];
+#pragma unroll
+    for (int k = 0; k < NQ; ++k) {
+        const int n0 = (k * S + s) * 4;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) A2[4 * k + j] = 0.f;
         if (VEC4) {
-            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-            const bool in = on && n0 < a.N;
-            if (in) f = *reinterpret_cast<const float4*>(hp);
-            h[b][0] = f.x; h[b][1] = f.y; h[b][2] = f.z; h[b][3] = f.w;
-            unpack<T, 4>(in ? load_pack<4>(Bp) : zero_pack<T, 4>(), B[b]);
-            unpack<T, 4>(in ? load_pack<4>(Cp) : zero_pack<T, 4>(), C[b]);
+            if (live && n0 < a.N) unpack<float, 4>(load_pack<4>(a.A + (long long)d * a.N + n0), A2 + 4 * k);
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = on && n0 + j < a.N;
-                h[b][j] = in ? hp[j] : 0.f;
-                B[b][j] = in ? to_f32<T>(Bp[j]) : 0.f;
-                C[b][j] = in ? to_f32<T>(Cp[j]) : 0.f;
-            }
+            for (int j = 0; j < 4; ++j) A2[4 * k + j] = live && n0 + j < a.N ? a.A[(long long)d * a.N + n0 + j] : 0.f;
         }
-    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) A2[j] = live && n0 + j < a.N ? a.A[(long long)d * a.N + n0 + j] * kLog2e : 0.f;
+        for (int j = 0; j < 4; ++j) A2[4 * k + j] *= kLog2e;
+    }
     const float bias = a.delta_bias && live ? a.delta_bias[d] : 0.f;
     const float dsk = a.Dskip && live ? a.Dskip[d] : 0.f;
+    F2 dt2{v[0] + bias, v[1] + bias};
+    if (a.softplus) dt2 = softplus2(dt2);
+    const F2 zz{z[0], z[1]}, gate = mul2(zz, sigmoid2(zz));
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
         const long long q = q0 + b;
         const bool on = live && q < a.num_seqs;
-        float dt = v[b] + bias;
-        if (a.softplus) dt = softplus(dt);
-        const float u = dt * x[b];
-        float y = 0.f;
+        const float dt = b ? dt2.y : dt2.x, u = dt * x[b];
+        F2 acc{0.f, 0.f};
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            h[b][j] = fmaf(ex2(dt * A2[j]), h[b][j], u * B[b][j]);
-            y = fmaf(h[b][j], C[b][j], y);
+        for (int k = 0; k < NQ; ++k) {
+            float fb[4], fc[4];
+            unpack<T, 4>(B[b][k], fb);
+            unpack<T, 4>(C[b][k], fc);
+#pragma unroll
+            for (int j = 0; j < 4; j += 2) {
+                const int n = 4 * k + j;
+                const F2 e = ex2(mul2(both(dt), F2{A2[n], A2[n + 1]}));
+                const F2 o = fma2(e, F2{h[b][n], h[b][n + 1]}, mul2(both(u), F2{fb[j], fb[j + 1]}));
+                acc = fma2(o, F2{fc[j], fc[j + 1]}, acc);
+                h[b][n] = o.x;
+                h[b][n + 1] = o.y;
+            }
         }
+        float y = acc.x + acc.y;
 #pragma unroll
         for (int m = 1; m < S; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
         if (!on) continue;
-        float* hp = a.hT + (q * a.D + d) * a.N + n0;
-        if (VEC4) {
-            if (n0 < a.N) *reinterpret_cast<float4*>(hp) = make_float4(h[b][0], h[b][1], h[b][2], h[b][3]);
-        } else {
+        float* hp = a.hT + (q * a.D + d) * a.N;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (n0 + j < a.N) hp[j] = h[b][j];
+        for (int k = 0; k < NQ; ++k) {
+            const int n0 = (k * S + s) * 4;
+            if (VEC4) {
+                if (n0 < a.N)
+                    *reinterpret_cast<float4*>(hp + n0) = make_float4(h[b][4 * k], h[b][4 * k + 1], h[b][4 * k + 2], h[b][4 * k + 3]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n0 + j < a.N) hp[n0 + j] = h[b][4 * k + j];
+            }
         }
         if (s == 0) {
             y = fmaf(dsk, x[b], y);
-            if (a.z) y *= z[b] * sigmoid<sizeof(T) == 2>(z[b]);
+            if (a.z) y *= b ? gate.y : gate.x;
             static_cast<T*>(a.out)[q * a.D + d] = from_f32<T>(y);
         }
     }
@@ -466,21 +506,21 @@ cudaError_t fwd_t(const SsmArgs& a, cudaStream_t s) {
     return al ? fwd_n<T, true>(a, p, s) : fwd_n<T, false>(a, p, s);
 }
 
+template <typename T, int S, int NQ, bool VEC4>
+cudaError_t step_go(const SsmArgs& a, cudaStream_t s) {
+    const long long gx = ((long long)a.D * S + 255) / 256, gy = (a.num_seqs + 1) / 2;
+    if ((long long)a.D * S > 0xffffff00LL || gy > 65535) return cudaErrorInvalidConfiguration;
+    ssm_step_kernel<T, S, NQ, VEC4><<<dim3((unsigned)gx, (unsigned)gy), 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
 template <typename T, bool VEC4>
 cudaError_t step_n(const SsmArgs& a, cudaStream_t s) {
-    const int S = a.N <= 4 ? 1 : a.N <= 8 ? 2 : a.N <= 16 ? 4 : a.N <= 32 ? 8 : a.N <= 64 ? 16 : 32;
-    const long long gx = ((long long)a.D * S + 255) / 256, gy = (a.num_seqs + 3) / 4;
-    if (gx > 0x7fffffffLL || gy > 65535) return cudaErrorInvalidConfiguration;
-    const dim3 grid((unsigned)gx, (unsigned)gy);
-    switch (S) {
-        case 1: ssm_step_kernel<T, 1, VEC4><<<grid, 256, 0, s>>>(a); break;
-        case 2: ssm_step_kernel<T, 2, VEC4><<<grid, 256, 0, s>>>(a); break;
-        case 4: ssm_step_kernel<T, 4, VEC4><<<grid, 256, 0, s>>>(a); break;
-        case 8: ssm_step_kernel<T, 8, VEC4><<<grid, 256, 0, s>>>(a); break;
-        case 16: ssm_step_kernel<T, 16, VEC4><<<grid, 256, 0, s>>>(a); break;
-        default: ssm_step_kernel<T, 32, VEC4><<<grid, 256, 0, s>>>(a); break;
-    }
-    return cudaGetLastError();
+    if (a.N <= 4) return step_go<T, 1, 1, VEC4>(a, s);
+    if (a.N <= 8) return step_go<T, 1, 2, VEC4>(a, s);
+    if (a.N <= 16) return step_go<T, 2, 2, VEC4>(a, s);
+    if (a.N <= 32) return step_go<T, 4, 2, VEC4>(a, s);
+    if (a.N <= 64) return step_go<T, 8, 2, VEC4>(a, s);
+    return step_go<T, 16, 2, VEC4>(a, s);
 }
 
 }  // namespace
@@ -497,7 +537,7 @@ size_t ssm_fwd_workspace_bytes(long long B, long long T, int D, int N, int G, bo
 
 cudaError_t launch_ssm_step(const SsmArgs& a, bool bf16, cudaStream_t s) {
     const int b4 = bf16 ? 8 : 16, el = b4 / 4;   // four states at a time
-    const bool v = a.N % 4 == 0 && vec_ok(a.hT, 16, 16) && vec_ok(a.Bm, a.bs * el, b4) && vec_ok(a.Cm, a.cs * el, b4);
+    const bool v = a.N % 4 == 0 && vec_ok(a.hT, 16, 16) && vec_ok(a.A, 16, 16) && vec_ok(a.Bm, a.bs * el, b4) && vec_ok(a.Cm, a.cs * el, b4);
     if (bf16) return v ? ssm::step_n<__nv_bfloat16, true>(a, s) : ssm::step_n<__nv_bfloat16, false>(a, s);
     return v ? ssm::step_n<float, true>(a, s) : ssm::step_n<float, false>(a, s);
 }

@@ -6,58 +6,6 @@
 namespace kda {
 namespace ssm {
 
-constexpr float kLog2e = 1.4426950408889634f;
-
-__device__ __forceinline__ float ex2(float v) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
-    return r;
-}
-
-// Two fp32 values in a register pair; one instruction works on both (the same roundings as
-// two scalar ones, half the issue slots).
-struct F2 {
-    float x, y;
-};
-__device__ __forceinline__ unsigned long long f2_bits(F2 a) {
-    unsigned long long r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
-    return r;
-}
-__device__ __forceinline__ F2 f2_of(unsigned long long v) {
-    F2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ F2 mul2(F2 a, F2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
-    return f2_of(r);
-}
-__device__ __forceinline__ F2 add2(F2 a, F2 b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
-    return f2_of(r);
-}
-__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
-    return f2_of(r);
-}
-__device__ __forceinline__ F2 both(float v) { return F2{v, v}; }
-__device__ __forceinline__ F2 ex2(F2 v) { return F2{ex2(v.x), ex2(v.y)}; }
-
-__device__ __forceinline__ F2 rcp(F2 v) {
-    F2 r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(v.x));
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(v.y));
-    return r;
-}
-
-// The functions of the step size and the gate work on pairs and take the hardware's exponential
-// and reciprocal: each within a few units, |v| log2(e) more through the exponent's rounding.
-__device__ __forceinline__ F2 sigmoid2(F2 v) { return rcp(add2(both(1.0f), ex2(mul2(v, both(-kLog2e))))); }
-
 // softplus(v) = max(v, 0) + log(1 + e), e = e^-|v| <= 1.  With s = e / (2 + e) <= 1/3,
 // log(1 + e) = 2 atanh(s) = 2 s (1 + s^2/3 + s^4/5 + ..): the series ends at s^14/15, whose
 // remainder is below 2e-9 of the sum, so the value keeps its relative accuracy where e is
