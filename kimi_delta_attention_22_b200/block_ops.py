@@ -171,9 +171,12 @@ _NULL = contextlib.nullcontext()
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
 def _on(device):
     """The device of the tensors as the current one, for the launch."""
-    return _NULL if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return _NULL if _current() == device.index else torch.cuda.device(device)
 
 
 def _stream(device):
@@ -182,10 +185,10 @@ def _stream(device):
     return torch.cuda.current_stream(device).cuda_stream
 
 
-def _out(given, what, shape, dtype, device):
-    """(tensor, pointer): the caller's buffer, checked, or a new one."""
+def _out(given, what, shape, dtype, device, like=None):
+    """(tensor, pointer): the caller's buffer, checked, or a new one (`like`: a tensor of its type and device)."""
     if given is None:
-        t = torch.empty(shape, dtype=dtype, device=device)
+        t = torch.empty(shape, dtype=dtype, device=device) if like is None else like.new_empty(shape)
         return t, t.data_ptr()
     return given, _want(given, what, shape, dtype, device)
 
@@ -226,7 +229,7 @@ def kda_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, silu: bool =
     B, T, N = _batch(x, cu_seqlens, dev)
     st = (N, max(W - 1, 0), D)
     sp = _want(state, "state", st, x.dtype, dev)
-    out, op = _out(out, "out", x.shape, x.dtype, dev)
+    out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     fp = None
     if final_state is not None or want_state:
         final_state, fp = _out(final_state, "final_state", st, x.dtype, dev)
@@ -249,7 +252,7 @@ def kda_conv_step(x, weight, state, bias=None, silu: bool = True, out=None, lib=
     if state is None:
         raise ValueError("state is required")
     sp = _want(state, "state", (N, max(W - 1, 0), D), x.dtype, dev)
-    out, op = _out(out, "out", x.shape, x.dtype, dev)
+    out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     sh = ConvShape(N, 1, D, N, W, _code(x, "x"), 0, int(bool(silu)), xs, None)
     lib = lib or _b.load_library()
     with _on(dev):
@@ -337,7 +340,7 @@ def kda_ssm_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlen
     Dc, N, G, st, p = _ssm_common(x, dt, A, B, C, D, z, dt_bias, dev, False)
     b, T, n = _batch(x, cu_seqlens, dev)
     hp = _want(h0, "h0", (n, Dc, N), torch.float32, dev)
-    out, op = _out(out, "out", x.shape, x.dtype, dev)
+    out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     tp = None
     if hT is not None or want_state:
         hT, tp = _out(hT, "hT", (n, Dc, N), torch.float32, dev)
@@ -361,7 +364,7 @@ def kda_ssm_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, softplus: bool
     if h is None:
         raise ValueError("h is required")
     hp = _want(h, "h", (n, Dc, N), torch.float32, dev)
-    out, op = _out(out, "out", x.shape, x.dtype, dev)
+    out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     sh = SsmShape(n, 1, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, None)
     lib = lib or _b.load_library()
     with _on(dev):
@@ -435,11 +438,11 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, w
     dev = _cuda(x, "x")
     rows, G, D, _, inner, w, b = _norm_common(x, weight, bias, dev)
     xs = _strided(x, "x", x.shape, x.dtype, dev, inner, G * D)
-    out, op = _out(out, "out", x.shape, x.dtype, dev)
+    out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     mean = rstd = mp = rp = None
     if want_stats:
-        mean, mp = _out(None, "mean", x.shape[:-1], torch.float32, dev)
-        rstd, rp = _out(None, "rstd", x.shape[:-1], torch.float32, dev)
+        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
+        mp, rp = mean.data_ptr(), rstd.data_ptr()
     sh = NormShape(rows, G, D, _code(x, "x"), float(eps), xs)
     lib = lib or _b.load_library()
     with _on(dev):

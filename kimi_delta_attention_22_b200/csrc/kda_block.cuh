@@ -322,6 +322,33 @@ __device__ __forceinline__ void silu_n(float* v) {
     for (int i = 0; i < VEC; ++i) v[i] *= s[i];
 }
 
+// Asynchronous copies into slots of shared memory that only the copying thread reads: rows are
+// under way without holding registers, and no barrier is needed.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
+// A pack in shared memory.
+template <typename T, int VEC>
+__device__ __forceinline__ Pack<T, VEC> lds_pack(const void* p) {
+    Pack<T, VEC> r;
+    if constexpr (VEC * sizeof(T) == 16) {
+        const uint4 v = *static_cast<const uint4*>(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else {
+        static_assert(VEC * sizeof(T) == 8, "8 or 16 bytes");
+        const uint2 v = *static_cast<const uint2*>(p);
+        r.w[0] = v.x; r.w[1] = v.y;
+    }
+    return r;
+}
+
 // Whether every access of VEC * el bytes at p + k * stride_bytes is aligned.
 inline bool vec_ok(const void* p, long long stride_bytes, int bytes) {
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) % (unsigned)bytes) == 0 && stride_bytes % bytes == 0);

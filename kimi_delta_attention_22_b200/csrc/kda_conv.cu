@@ -79,9 +79,16 @@ __device__ __forceinline__ void shift_in(float (*win)[VEC], const float* cur) {
     for (int v = 0; v < VEC; ++v) win[WM - 2][v] = cur[v];
 }
 
+constexpr int kU = 4;       // rows worked on together
+constexpr int kAhead = 4;   // groups of kU rows in the ring, one of them being worked on
+template <typename T, int VEC>
+constexpr int fwd_ring() { return VEC > 1 ? kAhead * kU * 256 * VEC * (int)sizeof(T) : 0; }
+
 template <typename T, int VEC, int WM, bool SILU>
-__global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int run, long long nruns) {
+__global__ void __launch_bounds__(256, WM <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs a, long long run, long long nruns) {
     constexpr bool kFast = sizeof(T) == 2;
+    extern __shared__ __align__(16) uint8_t ring_mem[];   // [kAhead][kU][thread]
+    T* ring = reinterpret_cast<T*>(ring_mem);
     const int nvec = a.D / VEC;
     const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long d0 = (idx % nvec) * VEC;
@@ -122,22 +129,40 @@ __global__ void __launch_bounds__(256) conv_fwd_kernel(ConvArgs a, int run, long
         if (!r.ok) { ++t; continue; }
         const long long stop = t1 < r.e ? t1 : r.e;
         load_window<T, VEC, WM>(a, r, t, d0, win);
-        constexpr int U = 4;   // rows in flight: the next four are loaded before these are worked on
-        Pack<T, VEC> nx[U];
-        if (t + U <= stop) {
+        const int quads = (int)((stop - t) / kU);
+        const T* px = x + t * a.xs;
+        if constexpr (VEC > 1) {   // kAhead - 1 groups of four rows under way
+            int at = 0;
+            auto ahead = [&](int q, int slot) {
+                if (q < quads) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) nx[u] = load_pack<VEC>(x + (t + u) * a.xs);
-        }
-        for (; t + U <= stop; t += U) {
-            Pack<T, VEC> cur[U];
+                    for (int u = 0; u < kU; ++u)
+                        copy_async<VEC * sizeof(T)>(&ring[((slot * kU + u) * 256 + threadIdx.x) * VEC], px + ((long long)q * kU + u) * a.xs);
+                }
+                copy_commit();
+            };
 #pragma unroll
-            for (int u = 0; u < U; ++u) cur[u] = nx[u];
-            if (t + 2 * U <= stop) {
+            for (int k = 0; k < kAhead - 1; ++k) ahead(k, k);
+#pragma unroll 1
+            for (int q = 0; q < quads; ++q, t += kU) {
+                copy_wait<kAhead - 2>();
+                Pack<T, VEC> cur[kU];
 #pragma unroll
-                for (int u = 0; u < U; ++u) nx[u] = load_pack<VEC>(x + (t + U + u) * a.xs);
+                for (int u = 0; u < kU; ++u) cur[u] = lds_pack<T, VEC>(&ring[((at * kU + u) * 256 + threadIdx.x) * VEC]);
+                ahead(q + kAhead - 1, at == 0 ? kAhead - 1 : at - 1);   // into the slot that the last turn read
+                at = at == kAhead - 1 ? 0 : at + 1;
+#pragma unroll
+                for (int u = 0; u < kU; ++u) emit(t + u, cur[u]);
             }
+            copy_wait<0>();
+        } else {
+            for (int q = 0; q < quads; ++q, t += kU) {
+                Pack<T, VEC> cur[kU];
 #pragma unroll
-            for (int u = 0; u < U; ++u) emit(t + u, cur[u]);
+                for (int u = 0; u < kU; ++u) cur[u] = load_pack<VEC>(x + (t + u) * a.xs);
+#pragma unroll
+                for (int u = 0; u < kU; ++u) emit(t + u, cur[u]);
+            }
         }
         for (; t < stop; ++t) emit(t, load_pack<VEC>(x + t * a.xs));
     }
@@ -179,10 +204,15 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
 // written as one partial sum per CTA.  A run needs dpre of up to WM - 1 rows behind it:
 // those are computed again (they belong to the next run's dw).
 constexpr int kBwdWarps = 8;
+constexpr int kBwdAhead = 3;
 
 template <typename T, typename TG, int VEC, int WM, bool SILU>
-__global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, int run, long long nruns, int K) {
+__global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, long long run, long long nruns, int K) {
     constexpr bool kFast = sizeof(T) == 2;
+    constexpr int NT = 32 * kBwdWarps;
+    extern __shared__ __align__(16) float red[];   // the ring of rows; at the end [kBwdWarps][WM + 1][VEC][32]
+    T* ring_x = reinterpret_cast<T*>(red);
+    TG* ring_g = reinterpret_cast<TG*>(ring_x + kBwdAhead * kU * NT * VEC);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const long long d0 = ((long long)blockIdx.x * 32 + lane) * VEC;
     const bool live = d0 < a.D;
@@ -205,18 +235,22 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
                 float win[WM - 1][VEC];
                 load_window<T, VEC, WM>(a, r, p0, d0, win);
                 float dp[WM][VEC] = {};   // dp[j] = dpre[t - j]
-                // row t enters; row s = t - (WM-1) has all of its gradients and leaves
-                auto leave = [&](long long t) {
+                // row t enters; row s = t - (WM-1) has all of its gradients and leaves.  `edge`: s may lie
+                // in front of the piece (the state's gradient, or another run's row) or be one of the
+                // last W - 1 rows, which the final state holds.
+                auto leave = [&](long long t, bool edge) {
                     const long long s = t - (WM - 1);
-                    T* to;
-                    if (s >= p0) to = dx + s * a.D;
-                    else if (p0 == r.b && dst != nullptr && s - r.b >= -(a.W - 1))
-                        to = dst + ((long long)r.q * (a.W - 1) + (a.W - 1) + (s - r.b)) * a.D + d0;
-                    else return;
+                    T* to = dx + s * a.D;
                     float g[VEC] = {};
-                    const long long k = s - r.e + (a.W - 1);   // the row is the final state's k-th
-                    if (dfin != nullptr && k >= 0)
-                        unpack<T, VEC>(load_pack<VEC>(dfin + ((long long)r.q * (a.W - 1) + k) * a.D + d0), g);
+                    if (edge) {
+                        if (s < p0) {
+                            if (p0 != r.b || dst == nullptr || s - r.b < -(a.W - 1)) return;
+                            to = dst + ((long long)r.q * (a.W - 1) + (a.W - 1) + (s - r.b)) * a.D + d0;
+                        }
+                        const long long k = s - r.e + (a.W - 1);   // the row is the final state's k-th
+                        if (dfin != nullptr && k >= 0)
+                            unpack<T, VEC>(load_pack<VEC>(dfin + ((long long)r.q * (a.W - 1) + k) * a.D + d0), g);
+                    }
 #pragma unroll
                     for (int j = 0; j < WM; ++j) fma_n<VEC>(wr[j], dp[j], g);
                     store_f32<T, VEC>(to, g);
@@ -229,8 +263,17 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
                         float pre[VEC], sg[VEC];
                         conv_pre<VEC, WM>(win, cf, wr, br, pre);
                         sigmoid_n<VEC, kFast>(pre, sg);
+                        if constexpr (VEC > 1) {
 #pragma unroll
-                        for (int v = 0; v < VEC; ++v) g[v] *= sg[v] * fmaf(pre[v], 1.0f - sg[v], 1.0f);
+                            for (int v = 0; v < VEC; v += 2) {
+                                const F2 q{sg[v], sg[v + 1]}, p{pre[v], pre[v + 1]};
+                                const F2 o = mul2(mul2(F2{g[v], g[v + 1]}, q), fma2(p, fma2(q, both(-1.0f), both(1.0f)), both(1.0f)));
+                                g[v] = o.x;
+                                g[v + 1] = o.y;
+                            }
+                        } else {
+                            g[0] *= sg[0] * fmaf(pre[0], 1.0f - sg[0], 1.0f);
+                        }
                     }
 #pragma unroll
                     for (int j = WM - 1; j > 0; --j)
@@ -247,35 +290,58 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
                     shift_in<VEC, WM>(win, cf);
                 };
                 long long t = p0;
-                constexpr int U = 4;   // the next four rows are loaded before these are worked on
-                Pack<T, VEC> nx[U];
-                Pack<TG, VEC> ng[U];
-                auto fetch = [&](long long at) {
+                const int quads = (int)((p1 - p0) / kU);
+                Pack<T, VEC> cx[kU];
+                Pack<TG, VEC> cg[kU];
+                auto ahead = [&](int q, int slot) {   // four rows of x and d_out into the ring
+                    if constexpr (VEC > 1) {
+                        if (q < quads) {
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        nx[u] = load_pack<VEC>(x + (at + u) * a.xs);
-                        ng[u] = load_pack<VEC>(dy + (at + u) * a.D);
+                            for (int u = 0; u < kU; ++u) {
+                                const long long at = p0 + (long long)q * kU + u;
+                                copy_async<VEC * sizeof(T)>(&ring_x[((slot * kU + u) * NT + threadIdx.x) * VEC], x + at * a.xs);
+                                copy_async<VEC * sizeof(TG)>(&ring_g[((slot * kU + u) * NT + threadIdx.x) * VEC], dy + at * a.D);
+                            }
+                        }
+                        copy_commit();
                     }
                 };
-                if (t + U <= p1) fetch(t);
-                for (; t + U <= p1; t += U) {
-                    Pack<T, VEC> cx[U];
-                    Pack<TG, VEC> cg[U];
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        cx[u] = nx[u];
-                        cg[u] = ng[u];
+                for (int k = 0; k < kBwdAhead - 1; ++k) ahead(k, k);
+                int slot = 0;
+#pragma unroll 1
+                for (int q = 0; q < quads; ++q, t += kU) {
+                    if constexpr (VEC > 1) copy_wait<kBwdAhead - 2>();
+#pragma unroll
+                    for (int u = 0; u < kU; ++u) {
+                        if constexpr (VEC > 1) {
+                            cx[u] = lds_pack<T, VEC>(&ring_x[((slot * kU + u) * NT + threadIdx.x) * VEC]);
+                            cg[u] = lds_pack<TG, VEC>(&ring_g[((slot * kU + u) * NT + threadIdx.x) * VEC]);
+                        } else {
+                            cx[u] = load_pack<VEC>(x + (t + u) * a.xs);
+                            cg[u] = load_pack<VEC>(dy + (t + u) * a.D);
+                        }
                     }
-                    if (t + 2 * U <= p1) fetch(t + U);
+                    ahead(q + kBwdAhead - 1, slot == 0 ? kBwdAhead - 1 : slot - 1);
+                    slot = slot == kBwdAhead - 1 ? 0 : slot + 1;
+                    if (q * kU >= WM - 1) {   // inside: s is a row of the piece, W or more in front of the end
 #pragma unroll
-                    for (int u = 0; u < U; ++u) {
-                        enter(cx[u], cg[u], true);
-                        leave(t + u);
+                        for (int u = 0; u < kU; ++u) {
+                            enter(cx[u], cg[u], true);
+                            leave(t + u, false);
+                        }
+                    } else {
+#pragma unroll
+                        for (int u = 0; u < kU; ++u) {
+                            enter(cx[u], cg[u], true);
+                            leave(t + u, true);
+                        }
                     }
                 }
+                if constexpr (VEC > 1) copy_wait<0>();
                 for (; t < p1; ++t) {
                     enter(load_pack<VEC>(x + t * a.xs), load_pack<VEC>(dy + t * a.D), true);
-                    leave(t);
+                    leave(t, true);
                 }
                 for (; t < p1 + WM - 1; ++t) {   // behind the piece: another run's rows, or past the sequence's end
                     if (t < r.e) {
@@ -288,7 +354,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) dp[0][v] = 0.f;
                     }
-                    leave(t);
+                    leave(t, true);
                 }
                 p0 = p1;
             }
@@ -304,7 +370,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
             }
         }
     }
-    extern __shared__ float red[];   // [kBwdWarps][WM + 1][VEC][32]
+    __syncthreads();   // every thread is done with its ring
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
 #pragma unroll
@@ -326,45 +392,48 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, in
     }
 }
 
-// Rows per thread of the forward: long runs re-read fewer halo rows (W - 1 per run),
-// short ones give more threads; as long as about 1024 threads per SM remain.
-int fwd_run(long long M, long long nvec) {
-    int run = 32;
-    while (run > 4 && nvec * ((M + run - 1) / run) < (long long)kSMs * 1024) run >>= 1;
-    return run;
+// Rows per thread of the forward: one run for each thread that is resident at once (three CTAs
+// per SM), so that the ring is filled once and the W - 1 rows in front of a run are few; at
+// least eight rows, however few that leaves to run.
+long long fwd_run(long long M, long long nvec) {
+    const long long run = (M * nvec + kSMs * 768LL - 1) / (kSMs * 768LL);
+    return run < 8 ? 8 : run;
 }
 
 struct BwdPlan {
-    int run, K;
-    long long nruns;
+    int K;
+    long long run, nruns;
 };
-// Rows per run and CTAs along the rows (each writes one partial sum of dw and db).
+// One run of consecutive rows per warp, as many CTAs as are resident at once (two per SM): the
+// rows divide evenly and the WM - 1 rows behind a run, computed twice, are few.
 BwdPlan bwd_plan(long long M, int D, int vec) {
     BwdPlan p;
     const long long nblk = (D + 32LL * vec - 1) / (32LL * vec);
-    p.run = 64;
-    while (p.run > 8 && nblk * ((M + p.run - 1) / p.run) < (long long)kSMs * 16) p.run >>= 1;
-    p.nruns = (M + p.run - 1) / p.run;
-    long long K = (kSMs * 3 + nblk - 1) / nblk;
-    const long long most = (p.nruns + kBwdWarps - 1) / kBwdWarps;
+    long long K = 2 * kSMs / nblk;
+    const long long most = (M + 16LL * kBwdWarps - 1) / (16LL * kBwdWarps);   // at least 16 rows per run
     if (K > most) K = most;
     p.K = (int)(K < 1 ? 1 : K);
+    p.run = (M + (long long)p.K * kBwdWarps - 1) / ((long long)p.K * kBwdWarps);
+    if (p.run < 1) p.run = 1;
+    p.nruns = (M + p.run - 1) / p.run;
     return p;
 }
 
 template <typename T, int VEC, bool SILU>
 cudaError_t fwd_w(const ConvArgs& a, cudaStream_t s) {
     const long long nvec = a.D / VEC;
-    const int run = fwd_run(a.M, nvec);
+    const long long run = fwd_run(a.M, nvec);
     const long long nruns = (a.M + run - 1) / run;
     const long long grid = (nvec * (nruns + a.num_seqs) + 255) / 256;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    switch (a.W) {
-        case 2: conv_fwd_kernel<T, VEC, 2, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
-        case 3: conv_fwd_kernel<T, VEC, 3, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
-        case 4: conv_fwd_kernel<T, VEC, 4, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
-        default: conv_fwd_kernel<T, VEC, 8, SILU><<<(unsigned)grid, 256, 0, s>>>(a, run, nruns); break;
-    }
+    constexpr int smem = fwd_ring<T, VEC>();
+    auto k = a.W == 2   ? conv_fwd_kernel<T, VEC, 2, SILU>
+             : a.W == 3 ? conv_fwd_kernel<T, VEC, 3, SILU>
+             : a.W == 4 ? conv_fwd_kernel<T, VEC, 4, SILU>
+                        : conv_fwd_kernel<T, VEC, 8, SILU>;
+    cudaError_t e;
+    if (smem > 0 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    k<<<(unsigned)grid, 256, smem, s>>>(a, run, nruns);
     return cudaGetLastError();
 }
 template <typename T, int VEC, bool SILU>
@@ -383,9 +452,14 @@ template <typename T, typename TG, int VEC, int WM, bool SILU>
 cudaError_t bwd_one(const ConvArgs& a, cudaStream_t s) {
     const BwdPlan p = bwd_plan(a.M, a.D, VEC);
     const dim3 grid((unsigned)((a.D + 32 * VEC - 1) / (32 * VEC)), (unsigned)p.K);
-    const size_t smem = sizeof(float) * kBwdWarps * (WM + 1) * VEC * 32;
-    conv_bwd_kernel<T, TG, VEC, WM, SILU><<<grid, 32 * kBwdWarps, smem, s>>>(a, p.run, p.nruns, p.K);
-    cudaError_t e = cudaGetLastError();
+    constexpr int sums = (int)sizeof(float) * kBwdWarps * (WM + 1) * VEC * 32;
+    constexpr int ring = VEC > 1 ? kBwdAhead * kU * 32 * kBwdWarps * VEC * (int)(sizeof(T) + sizeof(TG)) : 0;
+    constexpr int smem = sums > ring ? sums : ring;
+    auto k = conv_bwd_kernel<T, TG, VEC, WM, SILU>;
+    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    k<<<grid, 32 * kBwdWarps, smem, s>>>(a, p.run, p.nruns, p.K);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     return launch_colsum(a.part, p.K, (long long)a.D * a.W, a.dw, a.D, a.db, 0, nullptr, s);
 }

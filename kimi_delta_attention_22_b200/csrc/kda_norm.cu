@@ -19,11 +19,11 @@ namespace {
 // Sum of two values over the L lanes that share a row (L <= 32: lanes of a warp;
 // else the whole CTA of L threads, through shared memory; buf is two such areas used in turn).
 template <int L>
-__device__ __forceinline__ float2 row_sum(float x, float y, float2* buf, int& turn) {
+__device__ __forceinline__ float2 row_sum(float x, float y, float2* buf, int& turn, bool two = true) {
 #pragma unroll
     for (int m = (L < 32 ? L : 32) / 2; m > 0; m >>= 1) {
         x += __shfl_xor_sync(0xffffffffu, x, m);
-        y += __shfl_xor_sync(0xffffffffu, y, m);
+        if (two) y += __shfl_xor_sync(0xffffffffu, y, m);
     }
     if constexpr (L > 32) {
         constexpr int NW = L / 32;
@@ -47,7 +47,7 @@ __device__ __forceinline__ float2 row_sum(float x, float y, float2* buf, int& tu
 #pragma unroll
             for (int m = 16; m > 0; m >>= 1) {
                 x += __shfl_xor_sync(0xffffffffu, x, m);
-                y += __shfl_xor_sync(0xffffffffu, y, m);
+                if (two) y += __shfl_xor_sync(0xffffffffu, y, m);
             }
         }
     }
@@ -61,38 +61,62 @@ constexpr int cta_rows() { return L > 32 ? 1 : cta_threads<L>() / L; }
 template <int L>
 constexpr int block_threads() { return L > 32 ? L : 256; }
 
-// Rows in flight per group of lanes (short rows: the loads of two hide more latency).
-template <int L>
-constexpr int rows_per_group() { return L > 32 ? 1 : 2; }
+// Rows of one group that L lanes take together (short rows: the loads of four hide more
+// latency, and their weights are read once).
+template <int L, int NC>
+constexpr int rows_per_item() { return L > 32 ? 1 : NC > 1 ? 2 : 4; }
 
 __device__ __forceinline__ long long div_by(long long a, int b) {   // a >= 0; 32-bit where that is enough
     return a <= 0xffffffffLL ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
+// Parameters of an access' columns: fp32, at most 16 bytes at a time.
+template <int VEC>
+__device__ __forceinline__ void load_params(const float* p, float* o) {
+    constexpr int PV = VEC > 4 ? 4 : VEC;
+#pragma unroll
+    for (int v = 0; v < VEC; v += PV) unpack<float, PV>(load_pack<PV>(p + v), o + v);
+}
+template <int VEC>
+__device__ __forceinline__ F2 pair(const float* f, int v) { return F2{f[v], VEC > 1 ? f[VEC > 1 ? v + 1 : 0] : 0.f}; }
+
 template <typename T, int VEC, int L, int NC>
 __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a) {
-    constexpr int NI = rows_per_group<L>();
+    constexpr int NI = rows_per_item<L, NC>();
     __shared__ float2 buf[L > 32 ? 2 * (L / 32) : 1];
     int turn = 0;
     const int lane = threadIdx.x % L, sub = threadIdx.x / L;
-    const long long item0 = ((long long)blockIdx.x * cta_rows<L>() + sub) * NI, items = a.rows * a.G;
+    const long long idx = (long long)blockIdx.x * cta_rows<L>() + sub, mb = div_by(idx, a.G);
+    const int g = (int)(idx - mb * a.G);
+    const long long row0 = mb * NI;
     const float inv = 1.0f / (float)a.D;
+    const T* xg = static_cast<const T*>(a.x) + (long long)g * a.D;
     Pack<T, VEC> px[NI][NC];
-    int g[NI];
 #pragma unroll
     for (int r = 0; r < NI; ++r) {
-        const long long item = item0 + r < items ? item0 + r : 0, row = div_by(item, a.G);
-        g[r] = (int)(item - row * a.G);
-        const T* x = static_cast<const T*>(a.x) + row * a.xs + (long long)g[r] * a.D;
+        const bool live = row0 + r < a.rows;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = (c * L + lane) * VEC;
-            px[r][c] = d < a.D ? load_pack<VEC>(x + d) : zero_pack<T, VEC>();
+            px[r][c] = live && d < a.D ? load_pack<VEC>(xg + (row0 + r) * a.xs + d) : zero_pack<T, VEC>();
+        }
+    }
+    float w[NC][VEC], b[NC][VEC];
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+        const int d = (c * L + lane) * VEC;
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) {
+            w[c][v] = 1.f;
+            b[c][v] = 0.f;
+        }
+        if (NI > 1 && d < a.D) {   // one row: read when they are needed instead
+            if (a.w) load_params<VEC>(a.w + (long long)g * a.D + d, w[c]);
+            if (a.b) load_params<VEC>(a.b + (long long)g * a.D + d, b[c]);
         }
     }
 #pragma unroll
     for (int r = 0; r < NI; ++r) {
-        const long long item = item0 + r;
         float f[NC][VEC];
         float s = 0.f;
 #pragma unroll
@@ -101,40 +125,45 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
 #pragma unroll
             for (int v = 0; v < VEC; ++v) s += f[c][v];
         }
-        const float mean = row_sum<L>(s, 0.f, buf, turn).x * inv;
-        s = 0.f;
+        const float mean = row_sum<L>(s, 0.f, buf, turn, false).x * inv;
+        F2 q{0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             if ((c * L + lane) * VEC < a.D) {
+                if constexpr (VEC == 1) {
+                    f[c][0] -= mean;
+                    q.x = fmaf(f[c][0], f[c][0], q.x);
+                } else {
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) {
-                    f[c][v] -= mean;
-                    s = fmaf(f[c][v], f[c][v], s);
+                    for (int v = 0; v < VEC; v += 2) {
+                        const F2 o = add2(pair<VEC>(f[c], v), both(-mean));
+                        q = fma2(o, o, q);
+                        f[c][v] = o.x;
+                        f[c][v + 1] = o.y;
+                    }
                 }
             }
         }
-        const float rstd = rsqrtf(row_sum<L>(s, 0.f, buf, turn).x * inv + a.eps);
-        if (item >= items) continue;   // no exchange is skipped: the next row's come first of all again
+        const float rstd = rsqrtf(row_sum<L>(q.x + q.y, 0.f, buf, turn, false).x * inv + a.eps);
+        if (row0 + r >= a.rows) continue;   // no exchange is skipped: the next row's come first of all again
+        const long long item = (row0 + r) * a.G + g;
         T* out = static_cast<T*>(a.out) + item * a.D;
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = (c * L + lane) * VEC;
             if (d >= a.D) continue;
-            constexpr int PV = VEC > 4 ? 4 : VEC;   // parameters: fp32, at most 16 bytes at a time
+            if (NI == 1) {
+                if (a.w) load_params<VEC>(a.w + (long long)g * a.D + d, w[c]);
+                if (a.b) load_params<VEC>(a.b + (long long)g * a.D + d, b[c]);
+            }
+            if constexpr (VEC == 1) {
+                f[c][0] = fmaf(f[c][0] * rstd, w[c][0], b[c][0]);
+            } else {
 #pragma unroll
-            for (int v = 0; v < VEC; ++v) f[c][v] *= rstd;
-#pragma unroll
-            for (int v = 0; v < VEC; v += PV) {
-                float t[PV];
-                if (a.w) {
-                    unpack<float, PV>(load_pack<PV>(a.w + (long long)g[r] * a.D + d + v), t);
-#pragma unroll
-                    for (int k = 0; k < PV; ++k) f[c][v + k] *= t[k];
-                }
-                if (a.b) {
-                    unpack<float, PV>(load_pack<PV>(a.b + (long long)g[r] * a.D + d + v), t);
-#pragma unroll
-                    for (int k = 0; k < PV; ++k) f[c][v + k] += t[k];
+                for (int v = 0; v < VEC; v += 2) {
+                    const F2 o = fma2(mul2(pair<VEC>(f[c], v), both(rstd)), pair<VEC>(w[c], v), pair<VEC>(b[c], v));
+                    f[c][v] = o.x;
+                    f[c][v + 1] = o.y;
                 }
             }
             store_f32<T, VEC>(out + d, f[c]);
@@ -146,137 +175,151 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
     }
 }
 
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(dst)), "l"(src) : "memory");
-}
-
 // grid (K, G): CTA (k, g) walks rows k, k + K, .. (times the rows it holds at once) of group g.
 // RING: x and d_out of the next rows are copied ahead (STG - 1 rows) into slots of shared memory
-// that only the copying thread reads; without it the next row waits in registers.
+// that only the copying thread reads; without it the next row waits in registers.  A row is
+// gone over twice in registers as it was loaded, once for its sums and the parameters'
+// gradients, once for dx: unpacking again costs less than the registers of fp32 copies.
+// Threads per SM that the registers are held to where two accesses of a lane leave the choice:
+// three quarters of the warps hide a row's exchanges better than half of them with no spill.
+template <int VEC, int L, int NC>
+constexpr int bwd_threads() {
+    return NC * VEC <= 8 ? 1024 : NC == 2 && L > 32 && L <= 256 ? 768 : block_threads<L>() > 512 ? block_threads<L>() : 512;
+}
+
 template <typename T, int VEC, int L, int NC, bool RING>
-__global__ void __launch_bounds__(block_threads<L>()) norm_bwd_kernel(NormArgs a, int K) {
+__global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() / block_threads<L>()) norm_bwd_kernel(NormArgs a, int K) {
     constexpr int R = cta_rows<L>(), NT = block_threads<L>(), STG = 4;
     __shared__ float2 buf[L > 32 ? 2 * (L / 32) : 1];
     extern __shared__ __align__(16) uint4 ring[];   // [STG][2][NC][NT]
     int turn = 0;
     const int lane = threadIdx.x % L, sub = threadIdx.x / L;
     const int g = blockIdx.y;
-    const T* xg = static_cast<const T*>(a.x) + (long long)g * a.D;
-    const T* yg = static_cast<const T*>(a.d_out) + (long long)g * a.D;
     const long long step = (long long)K * R, gd = (long long)a.G * a.D;
     const float inv = 1.0f / (float)a.D;
+    const T* xg = static_cast<const T*>(a.x) + (long long)g * a.D + lane * VEC;
+    const T* yg = static_cast<const T*>(a.d_out) + (long long)g * a.D + lane * VEC;
+    T* og = static_cast<T*>(a.dx) + (long long)g * a.D + lane * VEC;
+    const float* wg = a.w + (long long)g * a.D + lane * VEC;
     float dw[NC][VEC] = {}, db[NC][VEC] = {};
-    float w[RING ? 1 : NC][VEC];   // RING: read from the cache again for every row, the registers are worth more
-    auto weight = [&](int c, float* o) {
-        const int d = (c * L + lane) * VEC;
-        constexpr int PV = VEC > 4 ? 4 : VEC;
-#pragma unroll
-        for (int v = 0; v < VEC; v += PV) {
-            if (d < a.D && a.w) {
-                unpack<float, PV>(load_pack<PV>(a.w + (long long)g * a.D + d + v), o + v);
-            } else {
-#pragma unroll
-                for (int k = 0; k < PV; ++k) o[v + k] = d < a.D ? 1.f : 0.f;
-            }
-        }
-    };
-    if constexpr (!RING) {
-#pragma unroll
-        for (int c = 0; c < NC; ++c) weight(c, w[c]);
-    }
+    constexpr bool kKeep = NC * VEC <= 16;   // the weights fit in registers
+    float wk[kKeep ? NC : 1][VEC];
     Pack<T, VEC> px[NC], pg[NC];
-    float mean = 0.f, rstd = 0.f;
-    auto ahead = [&](long long row, int st) {   // RING: a row's copies (nothing behind the last row)
+    auto in = [&](int c) { return (c * L + lane) * VEC < a.D; };
+    auto weights = [&](int c, float* o) {
+#pragma unroll
+        for (int v = 0; v < VEC; ++v) o[v] = 1.f;
+        if (a.w != nullptr && in(c)) load_params<VEC>(wg + c * L * VEC, o);
+    };
+    if constexpr (kKeep) {
+#pragma unroll
+        for (int c = 0; c < NC; ++c) weights(c, wk[c]);
+    }
+    // Every thread of the CTA makes the same number of turns (the sums meet in barriers).
+    const long long first = (long long)blockIdx.x * R + sub;
+    // running pointers: the row that is read (or copied ahead) next, the one that is written next
+    const T *xn = xg + first * a.xs, *yn = yg + first * gd;
+    T* on = og + first * gd;
+    const float *mn = a.mean + first * a.G + g, *rn = a.rstd + first * a.G + g;
+    long long left = first < a.rows ? (a.rows - first + step - 1) / step : 0;       // rows of this group of lanes
+    long long ahead_left = left;
+    auto ahead = [&](int st) {   // RING: the next row's copies (nothing behind the last row)
         if constexpr (RING) {
-            if (row < a.rows) {
+            if (ahead_left > 0) {
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    const int d = (c * L + lane) * VEC;
-                    if (d < a.D) {
-                        copy16(&ring[((st * 2 + 0) * NC + c) * NT + threadIdx.x], xg + row * a.xs + d);
-                        copy16(&ring[((st * 2 + 1) * NC + c) * NT + threadIdx.x], yg + row * gd + d);
-                    }
+                    if (!in(c)) continue;
+                    copy_async<16>(&ring[((st * 2 + 0) * NC + c) * NT + threadIdx.x], xn + c * L * VEC);
+                    copy_async<16>(&ring[((st * 2 + 1) * NC + c) * NT + threadIdx.x], yn + c * L * VEC);
                 }
+                xn += step * a.xs;
+                yn += step * gd;
+                --ahead_left;
             }
-            asm volatile("cp.async.commit_group;" ::: "memory");
+            copy_commit();
         }
     };
-    auto fetch = [&](long long row, int st) {   // row's x, d_out into registers
-        const bool live = row < a.rows;
-        if constexpr (RING) asm volatile("cp.async.wait_group %0;" ::"n"(STG - 2) : "memory");
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-            const int d = (c * L + lane) * VEC;
-            const bool in = live && d < a.D;
-            px[c] = pg[c] = zero_pack<T, VEC>();
-            if constexpr (RING) {
-                if (in) {
-                    const uint4 u = ring[((st * 2 + 0) * NC + c) * NT + threadIdx.x], v = ring[((st * 2 + 1) * NC + c) * NT + threadIdx.x];
-                    px[c].w[0] = u.x; px[c].w[1] = u.y; px[c].w[2] = u.z; px[c].w[3] = u.w;
-                    pg[c].w[0] = v.x; pg[c].w[1] = v.y; pg[c].w[2] = v.z; pg[c].w[3] = v.w;
-                }
-            } else if (in) {
-                px[c] = load_pack<VEC>(xg + row * a.xs + d);
-                pg[c] = load_pack<VEC>(yg + row * gd + d);
-            }
-        }
-    };
-    auto stats = [&](long long row) {
-        const bool live = row < a.rows;
-        mean = live ? __ldg(a.mean + row * a.G + g) : 0.f;
-        rstd = live ? __ldg(a.rstd + row * a.G + g) : 0.f;
-    };
-    // Every thread of the CTA makes the same number of turns (the sums meet in barriers).
-    const long long first = (long long)blockIdx.x * R;
-    int st = 0;
     if constexpr (RING) {
 #pragma unroll
-        for (int k = 0; k < STG - 1; ++k) ahead(first + sub + k * step, k);
-    } else {
-        fetch(first + sub, 0);
+        for (int k = 0; k < STG - 1; ++k) ahead(k);
     }
-    stats(first + sub);
-    for (long long base = first; base < a.rows; base += step) {
-        const long long row = base + sub;
-        if constexpr (RING) {
-            fetch(row, st);
-            ahead(row + (STG - 1) * step, (st + STG - 1) % STG);   // into the slot that the last turn read
-            st = (st + 1) % STG;
-        }
-        float xh[NC][VEC], gy[NC][VEC];
-        float s1 = 0.f, s2 = 0.f;
-        const float rs = rstd, mu = mean;
-        stats(row + step);
+    float mean = left > 0 ? __ldg(mn) : 0.f, rstd = left > 0 ? __ldg(rn) : 0.f;
+    int st = 0;
+    for (long long base = (long long)blockIdx.x * R; base < a.rows; base += step, --left) {
+        const bool live = left > 0;
+        if constexpr (RING) copy_wait<STG - 2>();
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            unpack<T, VEC>(px[c], xh[c]);
-            unpack<T, VEC>(pg[c], gy[c]);
-            float wr[VEC];
-            if constexpr (RING) weight(c, wr);
-#pragma unroll
-            for (int v = 0; v < VEC; ++v) {
-                xh[c][v] = (xh[c][v] - mu) * rs;
-                dw[c][v] = fmaf(gy[c][v], xh[c][v], dw[c][v]);
-                db[c][v] += gy[c][v];
-                gy[c][v] *= RING ? wr[v] : w[RING ? 0 : c][v];   // 0 behind the row's end
-                s1 += gy[c][v];
-                s2 = fmaf(gy[c][v], xh[c][v], s2);
+            px[c] = pg[c] = zero_pack<T, VEC>();
+            if (!live || !in(c)) continue;
+            if constexpr (RING) {
+                px[c] = lds_pack<T, VEC>(&ring[((st * 2 + 0) * NC + c) * NT + threadIdx.x]);
+                pg[c] = lds_pack<T, VEC>(&ring[((st * 2 + 1) * NC + c) * NT + threadIdx.x]);
+            } else {
+                px[c] = load_pack<VEC>(xn + c * L * VEC);
+                pg[c] = load_pack<VEC>(yn + c * L * VEC);
             }
         }
-        if constexpr (!RING) fetch(row + step, 0);   // under way while this row's sums meet
-        const float2 t = row_sum<L>(s1, s2, buf, turn);
-        const float c1 = t.x * inv, c2 = t.y * inv;
-        if (row < a.rows) {
-            T* dx = static_cast<T*>(a.dx) + (row * a.G + g) * a.D;
+        if constexpr (RING) {
+            ahead(st == 0 ? STG - 1 : st - 1);   // into the slot that the last turn read
+            st = st == STG - 1 ? 0 : st + 1;
+        } else {
+            xn += step * a.xs;
+            yn += step * gd;
+        }
+        const float rs = rstd, mu = mean;
+        mn += step * a.G;
+        rn += step * a.G;
+        if (left > 1) {
+            mean = __ldg(mn);
+            rstd = __ldg(rn);
+        }
+        F2 s1{0.f, 0.f}, s2{0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            if (!in(c)) continue;
+            float x[VEC], y[VEC], wr[VEC];
+            unpack<T, VEC>(px[c], x);
+            unpack<T, VEC>(pg[c], y);
+            if constexpr (!kKeep) weights(c, wr);
+            const float* w = kKeep ? wk[kKeep ? c : 0] : wr;
+#pragma unroll
+            for (int v = 0; v < VEC; v += (VEC > 1 ? 2 : 1)) {
+                const F2 xh = mul2(add2(pair<VEC>(x, v), both(-mu)), both(rs)), gy = pair<VEC>(y, v);
+                const F2 nw = fma2(gy, xh, pair<VEC>(dw[c], v)), nb = add2(gy, pair<VEC>(db[c], v));
+                dw[c][v] = nw.x;
+                db[c][v] = nb.x;
+                if (VEC > 1) {
+                    dw[c][VEC > 1 ? v + 1 : 0] = nw.y;
+                    db[c][VEC > 1 ? v + 1 : 0] = nb.y;
+                }
+                const F2 gw = mul2(gy, pair<VEC>(w, v));
+                s1 = add2(s1, gw);
+                s2 = fma2(gw, xh, s2);
+            }
+        }
+        const float2 t = row_sum<L>(VEC > 1 ? s1.x + s1.y : s1.x, VEC > 1 ? s2.x + s2.y : s2.x, buf, turn);
+        if (live) {
+            // rstd (gw - c1 - xhat c2) = gw rstd + (x k2 + k1), k2 = -c2 rstd^2, k1 = -c1 rstd - mean k2
+            const float k2 = -t.y * inv * rs * rs, k1 = fmaf(-mu, k2, -t.x * inv * rs);
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
-                const int d = (c * L + lane) * VEC;
-                if (d >= a.D) continue;
-                float o[VEC];
+                if (!in(c)) continue;
+                float x[VEC], y[VEC], wr[VEC];
+                unpack<T, VEC>(px[c], x);
+                unpack<T, VEC>(pg[c], y);
+                if constexpr (!kKeep) weights(c, wr);
+                const float* w = kKeep ? wk[kKeep ? c : 0] : wr;
 #pragma unroll
-                for (int v = 0; v < VEC; ++v) o[v] = rs * (gy[c][v] - c1 - xh[c][v] * c2);
-                store_f32<T, VEC>(dx + d, o);
+                for (int v = 0; v < VEC; v += (VEC > 1 ? 2 : 1)) {
+                    const F2 gw = mul2(pair<VEC>(y, v), pair<VEC>(w, v));
+                    const F2 o = fma2(gw, both(rs), fma2(pair<VEC>(x, v), both(k2), both(k1)));
+                    x[v] = o.x;
+                    if (VEC > 1) x[VEC > 1 ? v + 1 : 0] = o.y;
+                }
+                store_f32<T, VEC>(on + c * L * VEC, x);
             }
+            on += step * gd;
         }
     }
     if (a.part == nullptr) return;
@@ -349,18 +392,17 @@ int bwd_ctas(long long rows, int G, int rows_per_cta, int threads, int sm_thread
 
 template <typename T, int VEC, int L, int NC>
 cudaError_t fwd_one(const NormArgs& a, cudaStream_t s) {
-    const long long items = a.rows * a.G;
-    constexpr int per = cta_rows<L>() * rows_per_group<L>();
-    const long long grid = (items + per - 1) / per;
+    constexpr int NI = rows_per_item<L, NC>();
+    const long long items = (a.rows + NI - 1) / NI * a.G, grid = (items + cta_rows<L>() - 1) / cta_rows<L>();
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     norm_fwd_kernel<T, VEC, L, NC><<<(unsigned)grid, block_threads<L>(), 0, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int VEC, int L, int NC>
 cudaError_t bwd_one(const NormArgs& a, cudaStream_t s) {
-    constexpr bool RING = VEC > 1 && NC * block_threads<L>() * 128 <= 128 * 1024;
+    constexpr bool RING = VEC > 1 && NC * block_threads<L>() * 128 <= 200 * 1024;
     constexpr int smem = RING ? NC * block_threads<L>() * 128 : 0;   // 4 rows' x and d_out
-    const int K = bwd_ctas(a.rows, a.G, cta_rows<L>(), block_threads<L>(), NC * VEC >= 16 ? 512 : 1024);
+    const int K = bwd_ctas(a.rows, a.G, cta_rows<L>(), block_threads<L>(), bwd_threads<VEC, L, NC>());
     auto k = norm_bwd_kernel<T, VEC, L, NC, RING>;
     cudaError_t e;
     if (smem > 0 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
@@ -393,11 +435,19 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
         if (n <= 16) KDA_NORM(V, 16, 1);
         if (n <= 32) KDA_NORM(V, 32, 1);
         if (n <= 64) KDA_NORM(V, 32, 2);
-        if (n <= 128) KDA_NORM(V, 128, 1);
-        if (n <= 256) KDA_NORM(V, 256, 1);
-        if (n <= 512) KDA_NORM(V, 256, 2);
-        if (n <= 1024) KDA_NORM(V, 512, 2);
-        if (n <= 2048) KDA_NORM(V, 1024, 2);
+        if constexpr (BWD) {   // longer runs per lane: the row's sums and copies cost the same for each lane
+            if (n <= 128) KDA_NORM(V, 64, 2);
+            if (n <= 256) KDA_NORM(V, 128, 2);
+            if (n <= 512) KDA_NORM(V, 256, 2);
+            if (n <= 1024) KDA_NORM(V, 512, 2);
+            if (n <= 2048) KDA_NORM(V, 512, 4);
+        } else {
+            if (n <= 128) KDA_NORM(V, 128, 1);
+            if (n <= 256) KDA_NORM(V, 256, 1);
+            if (n <= 512) KDA_NORM(V, 256, 2);
+            if (n <= 1024) KDA_NORM(V, 512, 2);
+            if (n <= 2048) KDA_NORM(V, 1024, 2);
+        }
         if constexpr (V == 4) {
             if (n <= 4096) KDA_NORM(V, 1024, 4);
             KDA_NORM(V, 1024, 8);
@@ -432,7 +482,7 @@ cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t s) {
 
 // The partial sums of the most CTAs that any layout of the row would use.
 size_t norm_bwd_workspace_bytes(long long rows, int G, int D) {
-    return sizeof(float) * 2 * (size_t)G * D * bwd_ctas(rows, G, 1, 128, 1024);
+    return sizeof(float) * 2 * (size_t)G * D * bwd_ctas(rows, G, 1, 64, 1024);
 }
 
 }  // namespace kda

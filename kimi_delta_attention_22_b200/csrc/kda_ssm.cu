@@ -49,13 +49,13 @@ __device__ __forceinline__ void bar_arrive(int b) {
 
 template <typename T, int S, int NS, bool ALIGNED, bool SUMMARY>
 __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Segments seg, int nblk, float* hseg, float* dtseg) {
-    constexpr int CH = kThreads / S, TT = tile_rows<S>(), LD = TT + 4, NP = S * NS;
+    constexpr int CH = kThreads / S, TT = tile_rows<S>(), NP = S * NS;
     constexpr int VPR = CH / 8;                 // threads per staged row
     constexpr int BPT = (TT * NP + kThreads - 1) / kThreads;   // staged elements of B (and C) per thread
     constexpr bool kAhead = BPT <= 8;           // B and C of the next tile wait in registers
     static_assert(TT * VPR <= kThreads && TT % 4 == 0, "tile");
     extern __shared__ __align__(16) float sm[];   // two tile buffers
-    constexpr int kBuf = (SUMMARY ? 2 : 3) * CH * LD + (SUMMARY ? 1 : 2) * TT * NP;
+    constexpr int kBuf = (SUMMARY ? 2 : 3) * CH * TT + (SUMMARY ? 1 : 2) * TT * NP;
 
     const long long sg = blockIdx.x / nblk;   // segment, or behind them
     const ChannelBlock cb = channel_block<CH>(blockIdx.x % nblk, a.D, a.G);
@@ -117,13 +117,10 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
                 }
             }
         };
-        auto one = [](const Pack<T, 1>& p) {
-            float f;
-            unpack<T, 1>(p, &f);
-            return f;
-        };
+        auto put = [](float* to, const Pack<T, 1>& p) { unpack<T, 1>(p, to); };
         auto lay = [&](long long tile, float* buf) {   // the fetched tile into a buffer
-            float *s_dt = buf, *s_u = s_dt + CH * LD, *s_B = s_u + (SUMMARY ? 1 : 2) * CH * LD, *s_C = s_B + TT * NP;
+            float *s_dt = buf, *s_u = s_dt + CH * TT;
+            float *s_B = s_u + (SUMMARY ? 1 : 2) * CH * TT, *s_C = s_B + TT * NP;
             if (stager) {
                 float x[8], v[8];
                 unpack<T, 8>(nx, x);
@@ -133,27 +130,27 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
                     F2 dt = add2(F2{v[i], v[i + 1]}, F2{bias[i], bias[i + 1]});
                     if (a.softplus) dt = softplus2(dt);
                     const F2 u = mul2(dt, F2{x[i], x[i + 1]});
-                    s_dt[(sc0 + i) * LD + srow] = dt.x;
-                    s_dt[(sc0 + i + 1) * LD + srow] = dt.y;
-                    s_u[(sc0 + i) * LD + srow] = u.x;
-                    s_u[(sc0 + i + 1) * LD + srow] = u.y;
+                    s_dt[cell<TT>(sc0 + i, srow)] = dt.x;
+                    s_dt[cell<TT>(sc0 + i + 1, srow)] = dt.y;
+                    s_u[cell<TT>(sc0 + i, srow)] = u.x;
+                    s_u[cell<TT>(sc0 + i + 1, srow)] = u.y;
                 }
             }
 #pragma unroll
             for (int e = 0; e < BPT; ++e) {
                 if (e * kThreads + tid >= TT * NP) continue;
                 if constexpr (kAhead) {
-                    s_B[e * kThreads + tid] = one(nB[e]);
-                    if (!SUMMARY) s_C[e * kThreads + tid] = one(nC[e]);
+                    put(s_B + e * kThreads + tid, nB[e]);
+                    if (!SUMMARY) put(s_C + e * kThreads + tid, nC[e]);
                 } else {
-                    s_B[e * kThreads + tid] = one(bc(Bp, a.bs, tile, e));
-                    if (!SUMMARY) s_C[e * kThreads + tid] = one(bc(Cp, a.cs, tile, e));
+                    put(s_B + e * kThreads + tid, bc(Bp, a.bs, tile, e));
+                    if (!SUMMARY) put(s_C + e * kThreads + tid, bc(Cp, a.cs, tile, e));
                 }
             }
         };
         auto emit = [&](long long tile, const float* buf, const Pack<T, 8>& cx, const Pack<T, 8>& cz) {
             if constexpr (!SUMMARY) {
-                const float* s_y = buf + 2 * CH * LD;
+                const float* s_y = buf + 2 * CH * TT;
                 if (!r.ok || tile >= r.e) r = find_seq(a.cu, a.num_seqs, a.M, a.T, tile);
                 if (!stager || tile + srow >= t1) return;
                 if (r.ok && tile + srow < r.e ? false : !find_seq(a.cu, a.num_seqs, a.M, a.T, tile + srow).ok) return;
@@ -163,7 +160,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) {
                     F2 o = fma2(F2{dsk[i], dsk[i + 1]}, F2{x[i], x[i + 1]},
-                                F2{s_y[(sc0 + i) * LD + srow], s_y[(sc0 + i + 1) * LD + srow]});
+                                F2{s_y[cell<TT>(sc0 + i, srow)], s_y[cell<TT>(sc0 + i + 1, srow)]});
                     if (a.z) {
                         const F2 zz{z[i], z[i + 1]};
                         o = mul2(o, mul2(zz, sigmoid2(zz)));
@@ -229,23 +226,23 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
     int b = 0;
     for (long long tile = t0; tile < t1; tile += TT, b ^= 1) {
         float* buf = sm + b * kBuf;
-        const float *s_dt = buf, *s_u = s_dt + CH * LD, *s_B = s_u + (SUMMARY ? 1 : 2) * CH * LD, *s_C = s_B + TT * NP;
-        float* s_y = buf + 2 * CH * LD;
+        const float *s_dt = buf, *s_u = s_dt + CH * TT;
+        const float *s_B = s_u + (SUMMARY ? 1 : 2) * CH * TT, *s_C = s_B + TT * NP;
+        float* s_y = buf + 2 * CH * TT;
         auto row_step = [&](float dt, float u, int i) {   // one row of the tile; the lane's share of y
             F2 acc{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < NS; j += 4) {
-                const float4 b4 = *reinterpret_cast<const float4*>(&s_B[i * NP + s * NS + j]);
-                float4 c4 = b4;
-                if (!SUMMARY) c4 = *reinterpret_cast<const float4*>(&s_C[i * NP + s * NS + j]);
+                F2 B[2], C[2];
+                lds_quad(&s_B[i * NP + s * NS + j], B);
+                if (!SUMMARY) lds_quad(&s_C[i * NP + s * NS + j], C);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const F2 e = ex2(mul2(both(dt), F2{A2[j + 2 * m], A2[j + 2 * m + 1]}));
-                    const F2 ub = mul2(both(u), m ? F2{b4.z, b4.w} : F2{b4.x, b4.y});
-                    const F2 hn = fma2(e, F2{h[j + 2 * m], h[j + 2 * m + 1]}, ub);
+                    const F2 hn = fma2(e, F2{h[j + 2 * m], h[j + 2 * m + 1]}, mul2(both(u), B[m]));
                     h[j + 2 * m] = hn.x;
                     h[j + 2 * m + 1] = hn.y;
-                    if (!SUMMARY) acc = fma2(hn, m ? F2{c4.z, c4.w} : F2{c4.x, c4.y}, acc);
+                    if (!SUMMARY) acc = fma2(hn, C[m], acc);
                 }
             }
             if (SUMMARY) dtsum += dt;
@@ -257,24 +254,24 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
         if (rows == TT && r.ok && tile + TT <= r.e) {   // the tile lies in one sequence
 #pragma unroll 2
             for (int i = 0; i < TT; i += 4) {
-                const float4 d4 = *reinterpret_cast<const float4*>(&s_dt[ch * LD + i]);
-                const float4 u4 = *reinterpret_cast<const float4*>(&s_u[ch * LD + i]);
+                const float4 d4 = *reinterpret_cast<const float4*>(&s_dt[cell<TT>(ch, i)]);
+                const float4 u4 = *reinterpret_cast<const float4*>(&s_u[cell<TT>(ch, i)]);
                 const float dts[4] = {d4.x, d4.y, d4.z, d4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
                 float y[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) y[k] = row_step(dts[k], us[k], i + k);
-                if constexpr (!SUMMARY) lane_sum4<S>(y[0], y[1], y[2], y[3], s, &s_y[ch * LD + i]);
+                if constexpr (!SUMMARY) lane_sum4<S>(y[0], y[1], y[2], y[3], s, &s_y[cell<TT>(ch, i)]);
             }
             if (tile + TT == r.e) finish();
         } else {
             for (int i = 0; i < rows; ++i) {
                 if (!r.ok || tile + i >= r.e) enter(tile + i);
                 if (!r.ok) continue;   // a row of no sequence
-                float y = row_step(s_dt[ch * LD + i], s_u[ch * LD + i], i);
+                float y = row_step(s_dt[cell<TT>(ch, i)], s_u[cell<TT>(ch, i)], i);
                 if (!SUMMARY) {
 #pragma unroll
                     for (int m = 1; m < S; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-                    if (s == 0) s_y[ch * LD + i] = y;
+                    if (s == 0) s_y[cell<TT>(ch, i)] = y;
                 }
                 if (tile + i + 1 == r.e) finish();
             }
@@ -292,8 +289,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
 }
 template <int S, int NS, bool SUMMARY>
 constexpr int scan_smem() {
-    constexpr int CH = kThreads / S, TT = tile_rows<S>(), LD = TT + 4, NP = S * NS;
-    return 2 * (int)sizeof(float) * ((SUMMARY ? 2 : 3) * CH * LD + (SUMMARY ? 1 : 2) * TT * NP);
+    constexpr int CH = kThreads / S, TT = tile_rows<S>(), NP = S * NS;
+    return 2 * (int)sizeof(float) * ((SUMMARY ? 2 : 3) * CH * TT + (SUMMARY ? 1 : 2) * TT * NP);
 }
 
 // hseg[k] (the state that segment k alone ends with) -> the state that enters segment k.
@@ -321,7 +318,7 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a, Segments seg, 
 // S lanes per channel, NQ runs of four states per lane (one 16-byte access each where N is a
 // multiple of 4); a thread takes the same channel of two sequences, all of their loads first.
 template <typename T, int S, int NQ, bool VEC4>
-__global__ void __launch_bounds__(256) ssm_step_kernel(SsmArgs a) {
+__global__ void __launch_bounds__(256, 4) ssm_step_kernel(SsmArgs a) {
     constexpr int NB = 2;
     const unsigned i = blockIdx.x * 256u + threadIdx.x;
     const int s = (int)(i % S);

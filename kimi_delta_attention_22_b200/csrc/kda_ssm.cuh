@@ -25,6 +25,37 @@ __device__ __forceinline__ F2 softplus2(F2 v) {
 }
 __device__ __forceinline__ float softplus(float v) { return softplus2(F2{v, v}).x; }
 
+// Where row `row` of channel c lies in a tile array [channel][row]: groups of four rows stay
+// together (one 16-byte access) and are permuted by the channel, so that neither the staging
+// threads (the same channel of eight vectors, four rows) nor the scanning ones (eight
+// neighbouring channels, the same rows) meet in a bank.
+template <int TT>
+__device__ __forceinline__ int cell(int c, int row) {
+    return c * TT + ((((row >> 2) ^ (c >> 3) ^ c) & (TT / 4 - 1)) << 2 | (row & 3));
+}
+
+// A pair of B or C in shared memory (as stored, two bf16 or two fp32).
+__device__ __forceinline__ F2 lds_pair(const float* p) {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    return F2{v.x, v.y};
+}
+__device__ __forceinline__ F2 lds_pair(const __nv_bfloat16* p) {
+    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+    return F2{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+}
+
+// Four states of B or C at once.
+__device__ __forceinline__ void lds_quad(const float* p, F2* o) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    o[0] = F2{v.x, v.y};
+    o[1] = F2{v.z, v.w};
+}
+__device__ __forceinline__ void lds_quad(const __nv_bfloat16* p, F2* o) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    o[0] = F2{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)};
+    o[1] = F2{__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
+}
+
 // 8 consecutive channels of one row (those below `n`), as raw words.
 template <typename T, bool ALIGNED>
 __device__ __forceinline__ Pack<T, 8> load8(const T* p, int n) {

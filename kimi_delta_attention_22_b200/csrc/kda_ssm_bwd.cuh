@@ -50,15 +50,6 @@ constexpr int channels() { return 2 * kThreads / S; }
 template <int S>
 constexpr int tile_rows() { return S >= 4 ? 32 : 8 * S; }
 
-// Where row `row` of channel c lies in a tile array [channel][row]: groups of four rows stay
-// together (one 16-byte access) and are permuted by the channel, so that neither the staging
-// threads (the same channel of eight vectors, four rows) nor the scanning ones (eight
-// neighbouring channels, the same rows) meet in a bank.
-template <int TT>
-__device__ __forceinline__ int cell(int c, int row) {
-    return c * TT + ((((row >> 2) ^ (c >> 3) ^ c) & (TT / 4 - 1)) << 2 | (row & 3));
-}
-
 // First / last rows of sequences and rows of any sequence, one bit per row of the tile.
 struct Events {
     uint32_t first, last, in;
@@ -82,15 +73,6 @@ __device__ __forceinline__ Events find_events(const SsmArgs& a, long long t0, in
     return e;
 }
 
-// A pair of B or C in shared memory (as stored, two bf16 or two fp32).
-__device__ __forceinline__ F2 lds_pair(const float* p) {
-    const float2 v = *reinterpret_cast<const float2*>(p);
-    return F2{v.x, v.y};
-}
-__device__ __forceinline__ F2 lds_pair(const __nv_bfloat16* p) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
-    return F2{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
-}
 __device__ __forceinline__ F2 shfl2(F2 v, int m) {
     return F2{__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m)};
 }
