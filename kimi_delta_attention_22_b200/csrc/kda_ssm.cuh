@@ -44,17 +44,32 @@ __device__ __forceinline__ F2 lds_pair(const __nv_bfloat16* p) {
     return F2{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
 }
 
-// Four states of B or C at once.
-__device__ __forceinline__ void lds_quad(const float* p, F2* o) {
-    const float4 v = *reinterpret_cast<const float4*>(p);
-    o[0] = F2{v.x, v.y};
-    o[1] = F2{v.z, v.w};
-}
-__device__ __forceinline__ void lds_quad(const __nv_bfloat16* p, F2* o) {
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
-    o[0] = F2{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u)};
-    o[1] = F2{__uint_as_float(v.y << 16), __uint_as_float(v.y & 0xffff0000u)};
-}
+// Four states of B and of C as they lie in shared memory, side by side: [row][lane][B, C][4].
+template <typename T, bool BOTH>
+struct Quads {
+    uint32_t w[(BOTH ? 2 : 1) * sizeof(T)];
+    __device__ __forceinline__ void load(const T* p) {
+        constexpr int n = (BOTH ? 2 : 1) * (int)sizeof(T);   // words
+        if constexpr (n == 2) {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            w[0] = v.x; w[1] = v.y;
+        } else {
+#pragma unroll
+            for (int k = 0; k < n; k += 4) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[k / 4];
+                w[k] = v.x; w[k + 1] = v.y; w[k + 2] = v.z; w[k + 3] = v.w;
+            }
+        }
+    }
+    __device__ __forceinline__ F2 get(int which, int m) const {   // pair m of B (0) or C (1)
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t v = w[which * 2 + m];
+            return F2{__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u)};
+        } else {
+            return F2{__uint_as_float(w[which * 4 + 2 * m]), __uint_as_float(w[which * 4 + 2 * m + 1])};
+        }
+    }
+};
 
 // 8 consecutive channels of one row (those below `n`), as raw words.
 template <typename T, bool ALIGNED>

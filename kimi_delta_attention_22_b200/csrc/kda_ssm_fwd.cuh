@@ -1,4 +1,4 @@
-// kda_ssm.cu -- selective state space scan: forward over rows, and one row on a state.
+// kda_ssm_fwd.cuh -- selective state space scan: forward over rows, and one row on a state.
 //
 //   dt = softplus(delta + bias),  h[n] <- e^{dt A[n]} h[n] + dt x B[n]
 //   y = sum_n h[n] C[n] + Dskip x,  out = y silu(z)
@@ -22,6 +22,8 @@
 // last state and the sum of dt), a short pass joins them (the decay over a segment is
 // e^{A sum dt}), pass 2 scans again from the right state.  This doubles the exponentials, so
 // it is used only below one CTA per SM.
+#pragma once
+
 #include "kda_ssm.cuh"
 
 namespace kda {
@@ -55,7 +57,8 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
     constexpr bool kAhead = BPT <= 8;           // B and C of the next tile wait in registers
     static_assert(TT * VPR <= kThreads && TT % 4 == 0, "tile");
     extern __shared__ __align__(16) float sm[];   // two tile buffers
-    constexpr int kBuf = (SUMMARY ? 2 : 3) * CH * TT + (SUMMARY ? 1 : 2) * TT * NP;
+    constexpr int NBC = SUMMARY ? 1 : 2;        // B, or B and C side by side
+    constexpr int kBuf = (SUMMARY ? 2 : 3) * CH * TT + NBC * TT * NP * (int)sizeof(T) / 4;   // floats
 
     const long long sg = blockIdx.x / nblk;   // segment, or behind them
     const ChannelBlock cb = channel_block<CH>(blockIdx.x % nblk, a.D, a.G);
@@ -117,10 +120,12 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
                 }
             }
         };
-        auto put = [](float* to, const Pack<T, 1>& p) { unpack<T, 1>(p, to); };
+        auto put = [](T* s_bc, int k, int which, const Pack<T, 1>& p) {   // element k of B (0) or C (1), as it is
+            store_pack<T, 1>(s_bc + (k / 4 * NBC + which) * 4 + k % 4, p);
+        };
         auto lay = [&](long long tile, float* buf) {   // the fetched tile into a buffer
             float *s_dt = buf, *s_u = s_dt + CH * TT;
-            float *s_B = s_u + (SUMMARY ? 1 : 2) * CH * TT, *s_C = s_B + TT * NP;
+            T* s_bc = reinterpret_cast<T*>(s_u + (SUMMARY ? 1 : 2) * CH * TT);
             if (stager) {
                 float x[8], v[8];
                 unpack<T, 8>(nx, x);
@@ -140,11 +145,11 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
             for (int e = 0; e < BPT; ++e) {
                 if (e * kThreads + tid >= TT * NP) continue;
                 if constexpr (kAhead) {
-                    put(s_B + e * kThreads + tid, nB[e]);
-                    if (!SUMMARY) put(s_C + e * kThreads + tid, nC[e]);
+                    put(s_bc, e * kThreads + tid, 0, nB[e]);
+                    if (!SUMMARY) put(s_bc, e * kThreads + tid, 1, nC[e]);
                 } else {
-                    put(s_B + e * kThreads + tid, bc(Bp, a.bs, tile, e));
-                    if (!SUMMARY) put(s_C + e * kThreads + tid, bc(Cp, a.cs, tile, e));
+                    put(s_bc, e * kThreads + tid, 0, bc(Bp, a.bs, tile, e));
+                    if (!SUMMARY) put(s_bc, e * kThreads + tid, 1, bc(Cp, a.cs, tile, e));
                 }
             }
         };
@@ -227,22 +232,24 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
     for (long long tile = t0; tile < t1; tile += TT, b ^= 1) {
         float* buf = sm + b * kBuf;
         const float *s_dt = buf, *s_u = s_dt + CH * TT;
-        const float *s_B = s_u + (SUMMARY ? 1 : 2) * CH * TT, *s_C = s_B + TT * NP;
+        const T* s_bc = reinterpret_cast<const T*>(s_u + (SUMMARY ? 1 : 2) * CH * TT) + s * NS * NBC;
         float* s_y = buf + 2 * CH * TT;
-        auto row_step = [&](float dt, float u, int i) {   // one row of the tile; the lane's share of y
+        using Q = Quads<T, !SUMMARY>;
+        auto quads = [&](int i, Q* q) {   // this lane's B and C of row i
+#pragma unroll
+            for (int j = 0; j < NS / 4; ++j) q[j].load(s_bc + (i * NP + j * 4) * NBC);
+        };
+        auto row_step = [&](float dt, float u, const Q* q) {   // one row; the lane's share of y
             F2 acc{0.f, 0.f};
 #pragma unroll
             for (int j = 0; j < NS; j += 4) {
-                F2 B[2], C[2];
-                lds_quad(&s_B[i * NP + s * NS + j], B);
-                if (!SUMMARY) lds_quad(&s_C[i * NP + s * NS + j], C);
 #pragma unroll
                 for (int m = 0; m < 2; ++m) {
                     const F2 e = ex2(mul2(both(dt), F2{A2[j + 2 * m], A2[j + 2 * m + 1]}));
-                    const F2 hn = fma2(e, F2{h[j + 2 * m], h[j + 2 * m + 1]}, mul2(both(u), B[m]));
+                    const F2 hn = fma2(e, F2{h[j + 2 * m], h[j + 2 * m + 1]}, mul2(both(u), q[j / 4].get(0, m)));
                     h[j + 2 * m] = hn.x;
                     h[j + 2 * m + 1] = hn.y;
-                    if (!SUMMARY) acc = fma2(hn, C[m], acc);
+                    if constexpr (!SUMMARY) acc = fma2(hn, q[j / 4].get(1, m), acc);
                 }
             }
             if (SUMMARY) dtsum += dt;
@@ -252,14 +259,28 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
         const int rows = (int)(t1 - tile < TT ? t1 - tile : TT);
         if (!r.ok || tile >= r.e) enter(tile);
         if (rows == TT && r.ok && tile + TT <= r.e) {   // the tile lies in one sequence
+            // four rows at a time, the next four's operands on their way from shared memory
+            float4 nd = *reinterpret_cast<const float4*>(&s_dt[cell<TT>(ch, 0)]);
+            float4 nu = *reinterpret_cast<const float4*>(&s_u[cell<TT>(ch, 0)]);
+            Q nq[4][NS / 4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) quads(k, nq[k]);
 #pragma unroll 2
             for (int i = 0; i < TT; i += 4) {
-                const float4 d4 = *reinterpret_cast<const float4*>(&s_dt[cell<TT>(ch, i)]);
-                const float4 u4 = *reinterpret_cast<const float4*>(&s_u[cell<TT>(ch, i)]);
-                const float dts[4] = {d4.x, d4.y, d4.z, d4.w}, us[4] = {u4.x, u4.y, u4.z, u4.w};
+                const float dts[4] = {nd.x, nd.y, nd.z, nd.w}, us[4] = {nu.x, nu.y, nu.z, nu.w};
+                Q q[4][NS / 4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < NS / 4; ++j) q[k][j] = nq[k][j];
+                const int n = i + 4 < TT ? i + 4 : 0;   // behind the last four: the first again, unused
+                nd = *reinterpret_cast<const float4*>(&s_dt[cell<TT>(ch, n)]);
+                nu = *reinterpret_cast<const float4*>(&s_u[cell<TT>(ch, n)]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) quads(n + k, nq[k]);
                 float y[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) y[k] = row_step(dts[k], us[k], i + k);
+                for (int k = 0; k < 4; ++k) y[k] = row_step(dts[k], us[k], q[k]);
                 if constexpr (!SUMMARY) lane_sum4<S>(y[0], y[1], y[2], y[3], s, &s_y[cell<TT>(ch, i)]);
             }
             if (tile + TT == r.e) finish();
@@ -267,7 +288,9 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
             for (int i = 0; i < rows; ++i) {
                 if (!r.ok || tile + i >= r.e) enter(tile + i);
                 if (!r.ok) continue;   // a row of no sequence
-                float y = row_step(s_dt[cell<TT>(ch, i)], s_u[cell<TT>(ch, i)], i);
+                Q q[NS / 4];
+                quads(i, q);
+                float y = row_step(s_dt[cell<TT>(ch, i)], s_u[cell<TT>(ch, i)], q);
                 if (!SUMMARY) {
 #pragma unroll
                     for (int m = 1; m < S; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
@@ -287,10 +310,10 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
         if (s == 0) dtseg[sg * a.D + d] = dtsum;
     }
 }
-template <int S, int NS, bool SUMMARY>
+template <typename T, int S, int NS, bool SUMMARY>
 constexpr int scan_smem() {
     constexpr int CH = kThreads / S, TT = tile_rows<S>(), NP = S * NS;
-    return 2 * (int)sizeof(float) * ((SUMMARY ? 2 : 3) * CH * TT + (SUMMARY ? 1 : 2) * TT * NP);
+    return 2 * ((int)sizeof(float) * (SUMMARY ? 2 : 3) * CH * TT + (int)sizeof(T) * (SUMMARY ? 1 : 2) * TT * NP);
 }
 
 // hseg[k] (the state that segment k alone ends with) -> the state that enters segment k.
@@ -314,145 +337,47 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a, Segments seg, 
     }
 }
 
-// One row of every sequence: the fp32 state is read and written once, which bounds the step.
-// S lanes per channel, NQ runs of four states per lane (one 16-byte access each where N is a
-// multiple of 4); a thread takes the same channel of two sequences, all of their loads first.
-template <typename T, int S, int NQ, bool VEC4>
-__global__ void __launch_bounds__(256, 4) ssm_step_kernel(SsmArgs a) {
-    constexpr int NB = 2;
-    const unsigned i = blockIdx.x * 256u + threadIdx.x;
-    const int s = (int)(i % S);
-    const bool live = i / S < (unsigned)a.D;
-    const int d = live ? (int)(i / S) : 0;
-    const int g = a.G == 1 ? 0 : d / (a.D / a.G);
-    const long long q0 = (long long)blockIdx.y * NB;
-    float h[NB][NQ * 4], x[NB], v[NB], z[NB];
-    Pack<T, 4> B[NB][NQ], C[NB][NQ];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const long long q = q0 + b;
-        const bool on = live && q < a.num_seqs;
-        const float* hp = a.hT + (q * a.D + d) * a.N;
-        const T* Bp = static_cast<const T*>(a.Bm) + q * a.bs + (long long)g * a.N;
-        const T* Cp = static_cast<const T*>(a.Cm) + q * a.cs + (long long)g * a.N;
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-            const int n0 = (k * S + s) * 4;
-            B[b][k] = C[b][k] = zero_pack<T, 4>();
-            if (VEC4) {
-                float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (on && n0 < a.N) {
-                    f = *reinterpret_cast<const float4*>(hp + n0);
-                    B[b][k] = load_pack<4>(Bp + n0);
-                    C[b][k] = load_pack<4>(Cp + n0);
-                }
-                h[b][4 * k] = f.x; h[b][4 * k + 1] = f.y; h[b][4 * k + 2] = f.z; h[b][4 * k + 3] = f.w;
-            } else {
-                float fb[4], fc[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const bool in = on && n0 + j < a.N;
-                    h[b][4 * k + j] = in ? hp[n0 + j] : 0.f;
-                    fb[j] = in ? to_f32<T>(Bp[n0 + j]) : 0.f;
-                    fc[j] = in ? to_f32<T>(Cp[n0 + j]) : 0.f;
-                }
-                B[b][k] = pack<T, 4>(fb);   // exact: they were of this type
-                C[b][k] = pack<T, 4>(fc);
-            }
-        }
-        x[b] = on ? to_f32<T>(static_cast<const T*>(a.x)[q * a.xs + d]) : 0.f;
-        v[b] = on ? to_f32<T>(static_cast<const T*>(a.delta)[q * a.ds + d]) : 0.f;
-        z[b] = on && a.z ? to_f32<T>(static_cast<const T*>(a.z)[q * a.zs + d]) : 0.f;
-    }
-    float A2[NQ * 4];
-#pragma unroll
-    for (int k = 0; k < NQ; ++k) {
-        const int n0 = (k * S + s) * 4;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) A2[4 * k + j] = 0.f;
-        if (VEC4) {
-            if (live && n0 < a.N) unpack<float, 4>(load_pack<4>(a.A + (long long)d * a.N + n0), A2 + 4 * k);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) A2[4 * k + j] = live && n0 + j < a.N ? a.A[(long long)d * a.N + n0 + j] : 0.f;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) A2[4 * k + j] *= kLog2e;
-    }
-    const float bias = a.delta_bias && live ? a.delta_bias[d] : 0.f;
-    const float dsk = a.Dskip && live ? a.Dskip[d] : 0.f;
-    F2 dt2{v[0] + bias, v[1] + bias};
-    if (a.softplus) dt2 = softplus2(dt2);
-    const F2 zz{z[0], z[1]}, gate = mul2(zz, sigmoid2(zz));
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        const long long q = q0 + b;
-        const bool on = live && q < a.num_seqs;
-        const float dt = b ? dt2.y : dt2.x, u = dt * x[b];
-        F2 acc{0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-            float fb[4], fc[4];
-            unpack<T, 4>(B[b][k], fb);
-            unpack<T, 4>(C[b][k], fc);
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const int n = 4 * k + j;
-                const F2 e = ex2(mul2(both(dt), F2{A2[n], A2[n + 1]}));
-                const F2 o = fma2(e, F2{h[b][n], h[b][n + 1]}, mul2(both(u), F2{fb[j], fb[j + 1]}));
-                acc = fma2(o, F2{fc[j], fc[j + 1]}, acc);
-                h[b][n] = o.x;
-                h[b][n + 1] = o.y;
-            }
-        }
-        float y = acc.x + acc.y;
-#pragma unroll
-        for (int m = 1; m < S; m <<= 1) y += __shfl_xor_sync(0xffffffffu, y, m);
-        if (!on) continue;
-        float* hp = a.hT + (q * a.D + d) * a.N;
-#pragma unroll
-        for (int k = 0; k < NQ; ++k) {
-            const int n0 = (k * S + s) * 4;
-            if (VEC4) {
-                if (n0 < a.N)
-                    *reinterpret_cast<float4*>(hp + n0) = make_float4(h[b][4 * k], h[b][4 * k + 1], h[b][4 * k + 2], h[b][4 * k + 3]);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (n0 + j < a.N) hp[n0 + j] = h[b][4 * k + j];
-            }
-        }
-        if (s == 0) {
-            y = fmaf(dsk, x[b], y);
-            if (a.z) y *= b ? gate.y : gate.x;
-            static_cast<T*>(a.out)[q * a.D + d] = from_f32<T>(y);
-        }
-    }
+// How the forward is laid out: lanes per channel, states per lane, segments.
+struct Plan {
+    int S, NS;
+    Segments seg;
+};
+int lanes_for(int N, int NS) {
+    int S = 1;
+    while (S * NS < N) S *= 2;
+    return S;
 }
-
-// Lanes per channel for N states (four, or eight states per lane above 32).
-int lanes_for(int N) { return N <= 4 ? 1 : N <= 8 ? 2 : N <= 16 ? 4 : N <= 64 ? 8 : 16; }
-int tile_for(int N) {
-    const int S = lanes_for(N);
-    return S >= 4 ? 32 : 8 * S;
-}
-
-// One segment per sequence of a dense batch (all rows of a packed one) as soon as that gives
-// a CTA per SM: cutting the rows costs a second set of exponentials.
-Segments plan(long long B, long long T, int D, int N, int G, bool varlen) {
+int states_for(int N, bool wide) { return wide || N > 32 ? 8 : 4; }
+// Eight states per lane take a fifth fewer instructions per state than four (fewer sums over
+// lanes, row operands read once for more states), but half as many CTAs: they are used where
+// those still fill the SMs (two CTAs each), or where the rows are cut, which gives as many CTAs
+// as are wanted.  One segment per sequence of a dense batch (all rows of a packed one) as soon as
+// four states per lane give a CTA per SM: cutting costs a second set of exponentials.
+// 4 x 2048 rows, 2048 channels, 16 states: 162 us whole; 32768 rows, 1024 channels: 489 us cut
+// with four states per lane, see the kernel for the figures with eight.
+Plan plan(long long B, long long T, int D, int N, int G, bool varlen) {
     const long long M = B * T, whole = varlen ? 1 : B;
-    const long long blocks = channel_blocks(D, G, kThreads / lanes_for(N));
-    Segments p{varlen ? M : T, whole, true};
-    if (blocks * whole >= kSMs) return p;
-    long long count = (4LL * kSMs + blocks - 1) / blocks;
-    const long long most = M / 128;   // at least 128 rows each
+    auto make = [&](bool wide) {
+        Plan p;
+        p.NS = states_for(N, wide);
+        p.S = lanes_for(N, p.NS);
+        p.seg = Segments{varlen ? M : T, whole, true};
+        return p;
+    };
+    auto blocks = [&](const Plan& p) { return channel_blocks(D, G, kThreads / p.S); };
+    Plan p = make(true);
+    if (blocks(p) * whole >= 2 * kSMs) return p;
+    const Plan narrow = make(false);
+    if (blocks(narrow) * whole >= kSMs) return narrow;
+    long long count = 2LL * kSMs / blocks(p);   // what is resident at once, and no more
+    const long long most = M / 128;             // at least 128 rows each
     if (count > most) count = most;
     if (count > 1024) count = 1024;
-    if (count <= 2 * whole) return p;   // at most twice the CTAs for twice the work
-    const int tile = tile_for(N);
-    p.len = ((M + count - 1) / count + tile - 1) / tile * tile;
-    p.count = (M + p.len - 1) / p.len;
-    p.whole = false;
+    if (count <= 2 * whole) return narrow;      // twice the CTAs would only pay for twice the work
+    const int tile = p.S >= 4 ? 32 : 8 * p.S;
+    p.seg.len = ((M + count - 1) / count + tile - 1) / tile * tile;
+    p.seg.count = (M + p.seg.len - 1) / p.seg.len;
+    p.seg.whole = false;
     return p;
 }
 
@@ -469,7 +394,7 @@ cudaError_t fwd_go(const SsmArgs& a, const Segments& p, cudaStream_t s) {
     cudaError_t e;
     if (!p.whole) {
         auto k = ssm_scan_kernel<T, S, NS, ALIGNED, true>;
-        constexpr int sm1 = scan_smem<S, NS, true>();
+        constexpr int sm1 = scan_smem<T, S, NS, true>();
         if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm1)) != cudaSuccess) return e;
         k<<<(unsigned)(blocks * p.count), 2 * kThreads, sm1, s>>>(a, p, nblk, hseg, dtseg);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -478,65 +403,41 @@ cudaError_t fwd_go(const SsmArgs& a, const Segments& p, cudaStream_t s) {
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
     auto k = ssm_scan_kernel<T, S, NS, ALIGNED, false>;
-    constexpr int sm2 = scan_smem<S, NS, false>();
+    constexpr int sm2 = scan_smem<T, S, NS, false>();
     if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm2)) != cudaSuccess) return e;
     k<<<(unsigned)(blocks * (p.count + extra)), 2 * kThreads, sm2, s>>>(a, p, nblk, hseg, dtseg);
     return cudaGetLastError();
 }
 
 template <typename T, bool ALIGNED>
-cudaError_t fwd_n(const SsmArgs& a, const Segments& p, cudaStream_t s) {
-    if (a.N <= 4) return fwd_go<T, 1, 4, ALIGNED>(a, p, s);
-    if (a.N <= 8) return fwd_go<T, 2, 4, ALIGNED>(a, p, s);
-    if (a.N <= 16) return fwd_go<T, 4, 4, ALIGNED>(a, p, s);
-    if (a.N <= 32) return fwd_go<T, 8, 4, ALIGNED>(a, p, s);
-    if (a.N <= 64) return fwd_go<T, 8, 8, ALIGNED>(a, p, s);
-    return fwd_go<T, 16, 8, ALIGNED>(a, p, s);
+cudaError_t fwd_n(const SsmArgs& a, const Plan& p, cudaStream_t s) {
+    if (p.NS == 4) {
+        switch (p.S) {
+            case 1: return fwd_go<T, 1, 4, ALIGNED>(a, p.seg, s);
+            case 2: return fwd_go<T, 2, 4, ALIGNED>(a, p.seg, s);
+            case 4: return fwd_go<T, 4, 4, ALIGNED>(a, p.seg, s);
+            default: return fwd_go<T, 8, 4, ALIGNED>(a, p.seg, s);
+        }
+    }
+    switch (p.S) {
+        case 1: return fwd_go<T, 1, 8, ALIGNED>(a, p.seg, s);
+        case 2: return fwd_go<T, 2, 8, ALIGNED>(a, p.seg, s);
+        case 4: return fwd_go<T, 4, 8, ALIGNED>(a, p.seg, s);
+        case 8: return fwd_go<T, 8, 8, ALIGNED>(a, p.seg, s);
+        default: return fwd_go<T, 16, 8, ALIGNED>(a, p.seg, s);
+    }
 }
 
 template <typename T>
 cudaError_t fwd_t(const SsmArgs& a, cudaStream_t s) {
     const int el = sizeof(T);
-    const Segments p = plan(a.T > 0 ? a.M / a.T : 0, a.T, a.D, a.N, a.G, a.cu != nullptr);
+    const Plan p = plan(a.T > 0 ? a.M / a.T : 0, a.T, a.D, a.N, a.G, a.cu != nullptr);
     const bool al = (a.D / a.G) % 8 == 0 && vec_ok(a.x, a.xs * el, 16) && vec_ok(a.delta, a.ds * el, 16) &&
                     vec_ok(a.z, a.zs * el, 16) && vec_ok(a.out, (long long)a.D * el, 16);
     return al ? fwd_n<T, true>(a, p, s) : fwd_n<T, false>(a, p, s);
 }
 
-template <typename T, int S, int NQ, bool VEC4>
-cudaError_t step_go(const SsmArgs& a, cudaStream_t s) {
-    const long long gx = ((long long)a.D * S + 255) / 256, gy = (a.num_seqs + 1) / 2;
-    if ((long long)a.D * S > 0xffffff00LL || gy > 65535) return cudaErrorInvalidConfiguration;
-    ssm_step_kernel<T, S, NQ, VEC4><<<dim3((unsigned)gx, (unsigned)gy), 256, 0, s>>>(a);
-    return cudaGetLastError();
-}
-template <typename T, bool VEC4>
-cudaError_t step_n(const SsmArgs& a, cudaStream_t s) {
-    if (a.N <= 4) return step_go<T, 1, 1, VEC4>(a, s);
-    if (a.N <= 8) return step_go<T, 1, 2, VEC4>(a, s);
-    if (a.N <= 16) return step_go<T, 2, 2, VEC4>(a, s);
-    if (a.N <= 32) return step_go<T, 4, 2, VEC4>(a, s);
-    if (a.N <= 64) return step_go<T, 8, 2, VEC4>(a, s);
-    return step_go<T, 16, 2, VEC4>(a, s);
-}
-
 }  // namespace
 }  // namespace ssm
-
-cudaError_t launch_ssm_fwd(const SsmArgs& a, bool bf16, cudaStream_t s) {
-    return bf16 ? ssm::fwd_t<__nv_bfloat16>(a, s) : ssm::fwd_t<float>(a, s);
-}
-
-size_t ssm_fwd_workspace_bytes(long long B, long long T, int D, int N, int G, bool varlen) {
-    const ssm::Segments p = ssm::plan(B, T, D, N, G, varlen);
-    return p.whole ? 0 : sizeof(float) * (size_t)p.count * D * (N + 1);
-}
-
-cudaError_t launch_ssm_step(const SsmArgs& a, bool bf16, cudaStream_t s) {
-    const int b4 = bf16 ? 8 : 16, el = b4 / 4;   // four states at a time
-    const bool v = a.N % 4 == 0 && vec_ok(a.hT, 16, 16) && vec_ok(a.A, 16, 16) && vec_ok(a.Bm, a.bs * el, b4) && vec_ok(a.Cm, a.cs * el, b4);
-    if (bf16) return v ? ssm::step_n<__nv_bfloat16, true>(a, s) : ssm::step_n<__nv_bfloat16, false>(a, s);
-    return v ? ssm::step_n<float, true>(a, s) : ssm::step_n<float, false>(a, s);
-}
 
 }  // namespace kda
