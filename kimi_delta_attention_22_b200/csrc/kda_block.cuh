@@ -113,7 +113,7 @@ struct SeqRange {
 __device__ __forceinline__ SeqRange find_seq(const int32_t* cu, int n, long long M, long long T, long long t) {
     SeqRange r;
     if (cu == nullptr) {
-        r.q = (int)(t / T);
+        r.q = t <= 0xffffffffLL ? (int)((unsigned)t / (unsigned)T) : (int)(t / T);   // t < M, T <= M
         r.b = (long long)r.q * T;
         r.e = r.b + T;
         r.ok = true;

@@ -54,11 +54,10 @@ constexpr int tile_rows() { return S >= 4 ? 32 : 8 * S; }
 struct Events {
     uint32_t first, last, in;
 };
-// r: a sequence met before (or none).  A tile inside it needs no search, the common case.
-__device__ __forceinline__ Events find_events(const SsmArgs& a, long long t0, int rows, SeqRange& r) {   // whole warps
+__device__ __forceinline__ Events find_events(const SsmArgs& a, long long t0, int rows) {   // whole warps
     Events e;
-    if (!r.ok || t0 < r.b || t0 >= r.e) r = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 < a.M ? t0 : a.M - 1);
-    if (r.ok && t0 >= r.b && t0 + rows <= r.e) {
+    const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 < a.M ? t0 : a.M - 1);
+    if (r.ok && t0 >= r.b && t0 + rows <= r.e) {   // the tile inside a sequence, the common case
         e.in = rows == 32 ? 0xffffffffu : (1u << rows) - 1;
         e.first = t0 == r.b ? 1u : 0u;
         e.last = t0 + rows == r.e ? 1u << (rows - 1) : 0u;
@@ -301,15 +300,8 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
             p[k][m] = F2{1.f, 1.f};
         }
     uint8_t f = 0;
-    float* ck[2];   // this thread's checkpoints, and its channels' sums of dt
-    float* dk[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        ck[k] = hck + (t0 / kSub * a.D + at.d[k]) * NP + at.s * 4;
-        dk[k] = dtck + t0 / kSub * a.D + at.d[k];
-    }
-    SeqRange seq{0, 0, 0, false};
-    Events ev = find_events(a, t0, TT, seq), evn{0, 0, 0};
+    float *ck = hck + t0 / kSub * a.D * NP, *dk = dtck + t0 / kSub * a.D;   // the next checkpoint
+    Events ev = find_events(a, t0, TT), evn{0, 0, 0};
     raw.load(a, cb, t0, ev.in);
     for (long long tile = t0; tile < t1; tile += TT, ev = evn) {
         if (tile == t0 && ((ev.first & 1) || !(ev.in & 1))) f |= kFirst;
@@ -320,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
         raw.template lay<true>(a, cb, tile, ev.in, s_dt, s_u, s_dy, s_B, s_C);
         __syncthreads();
         if (tile + TT < t1) {
-            evn = find_events(a, tile + TT, TT, seq);
+            evn = find_events(a, tile + TT, TT);
             raw.load(a, cb, tile + TT, evn.in);
         }
 #pragma unroll 1
@@ -329,13 +321,13 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (at.live[k]) {
-                    *reinterpret_cast<float2*>(ck[k] + 2 * at.sw) = make_float2(h[k][0].x, h[k][0].y);
-                    *reinterpret_cast<float2*>(ck[k] + 2 - 2 * at.sw) = make_float2(h[k][1].x, h[k][1].y);
-                    if (at.s == 0) *dk[k] = dtsum[k];
+                    *reinterpret_cast<float2*>(ck + at.d[k] * NP + at.n(0)) = make_float2(h[k][0].x, h[k][0].y);
+                    *reinterpret_cast<float2*>(ck + at.d[k] * NP + at.n(1)) = make_float2(h[k][1].x, h[k][1].y);
+                    if (at.s == 0) dk[at.d[k]] = dtsum[k];
                 }
-                ck[k] += (long long)a.D * NP;
-                dk[k] += a.D;
             }
+            ck += a.D * NP;
+            dk += a.D;
             auto rows = [&](auto evc) {   // eight rows, with or without sequences that begin or end there
                 constexpr bool EV = decltype(evc)::value;
 #pragma unroll
@@ -440,23 +432,23 @@ __global__ void __launch_bounds__(128) ssm_bwd_join_kernel(SsmArgs a, int NP, lo
     }
 }
 
-// The sums over a channel's S lanes of four rows' values v[slot][row], in place: channels are
-// exchanged first (in swapped order), then rows.  S = 1: all stay; S = 2: the lane has slot 0's
-// four rows; S >= 4: slot 0's rows 2 (s & 2) / 2 .. + 1 in v[0][0], v[0][1].
+// The sums over a channel's S lanes of four rows' values, in two steps.  Channels first, row by
+// row (the lanes of a pair hold the two channels in swapped order): of v[slot] the lane keeps slot
+// 0.  Then rows: S = 2 has all four; S >= 4 ends with rows 2 (s & 2) / 2 .. + 1 in r[0], r[1].
 template <int S>
-__device__ __forceinline__ void lane_sum42(const Place<S>& at, float (&v)[2][4]) {
-    if constexpr (S > 1) {
-        F2 lo = add2(F2{v[0][0], v[0][1]}, shfl2(F2{v[1][0], v[1][1]}, 1));
-        F2 hi = add2(F2{v[0][2], v[0][3]}, shfl2(F2{v[1][2], v[1][3]}, 1));
-        if constexpr (S > 2) {
-            const bool up = at.s & 2;   // keeps rows 2 and 3
-            F2 keep = up ? hi : lo;
-            keep = add2(keep, shfl2(up ? lo : hi, 2));
+__device__ __forceinline__ float channel_exchange(float v0, float v1) {
+    return v0 + __shfl_xor_sync(0xffffffffu, v1, 1);
+}
+template <int S>
+__device__ __forceinline__ void row_exchange(const Place<S>& at, float (&r)[4]) {
+    if constexpr (S > 2) {
+        const bool up = at.s & 2;   // keeps rows 2 and 3
+        F2 keep = up ? F2{r[2], r[3]} : F2{r[0], r[1]};
+        keep = add2(keep, shfl2(up ? F2{r[0], r[1]} : F2{r[2], r[3]}, 2));
 #pragma unroll
-            for (int m = 4; m < S; m <<= 1) keep = add2(keep, shfl2(keep, m));
-            lo = keep;
-        }
-        v[0][0] = lo.x; v[0][1] = lo.y; v[0][2] = hi.x; v[0][3] = hi.y;
+        for (int m = 4; m < S; m <<= 1) keep = add2(keep, shfl2(keep, m));
+        r[0] = keep.x;
+        r[1] = keep.y;
     }
 }
 
@@ -519,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
     const long long t0 = sg * seg.len, t1 = t0 + seg.len < a.M ? t0 + seg.len : a.M;
     // rows that the segment's incoming state reaches: those of the sequence it is cut out of
     const SeqRange r0 = find_seq(a.cu, a.num_seqs, a.M, a.T, t0);
-    const long long reach = r0.ok && r0.b < t0 ? r0.e : t0;
+    const int nrow = (int)(t1 - t0), reach = r0.ok && r0.b < t0 ? (int)(r0.e - t0 < nrow ? r0.e - t0 : nrow) : 0;
 
     F2 A2[2][2], dh[2][2], dA[2][2];
 #pragma unroll
@@ -532,24 +524,18 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
         }
     auto slot = [&](int which, int k, int m) { return s_ck + which * kCk + ((k * 2 + m) * kThreads + tid) * 2; };
     auto slot_dt = [&](int which, int k) { return s_ck + which * kCk + 8 * kThreads + k * kThreads + tid; };
-    const float* ck[2];   // the checkpoint that is fetched next
-    const float* dk[2];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        ck[k] = hck + ((t1 - 1) / kSub * a.D + at.d[k]) * NP + at.s * 4;
-        dk[k] = dtck + (t1 - 1) / kSub * a.D + at.d[k];
-    }
+    const float *ck = hck + (t1 - 1) / kSub * a.D * NP, *dk = dtck + (t1 - 1) / kSub * a.D;   // fetched next
     auto fetch = [&](int which) {
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             if (at.live[k]) {
-                cp_async8(slot(which, k, 0), ck[k] + 2 * at.sw);
-                cp_async8(slot(which, k, 1), ck[k] + 2 - 2 * at.sw);
-                cp_async4(slot_dt(which, k), dk[k]);
+                cp_async8(slot(which, k, 0), ck + at.d[k] * NP + at.n(0));
+                cp_async8(slot(which, k, 1), ck + at.d[k] * NP + at.n(1));
+                cp_async4(slot_dt(which, k), dk + at.d[k]);
             }
-            ck[k] -= (long long)a.D * NP;
-            dk[k] -= a.D;
         }
+        ck -= a.D * NP;
+        dk -= a.D;
     };
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -573,17 +559,16 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
     for (int k = 0; k < 2; ++k) skip[k] = a.Dskip && at.live[k] ? a.Dskip[at.d[k]] : 0.f;
     int phase = 0;
 
-    const long long last_tile = t0 + (t1 - t0 - 1) / TT * TT;
-    SeqRange seq = r0;
-    Events ev = find_events(a, last_tile, TT, seq), evn{0, 0, 0};
-    raw.load(a, cb, last_tile, ev.in);
-    float* bc = bcpart + ((long long)blk * a.M + last_tile) * 2 * a.N;   // the tile's dB, dC of this channel block
-    for (long long tile = last_tile; tile >= t0; tile -= TT, ev = evn, bc -= 2 * TT * (long long)a.N) {
-        raw.template lay<false>(a, cb, tile, ev.in, s_dt, s_x, s_dy, s_B, s_C);
+    const int last_tile = (nrow - 1) / TT * TT;   // rows count from the segment's first
+    Events ev = find_events(a, t0 + last_tile, TT), evn{0, 0, 0};
+    raw.load(a, cb, t0 + last_tile, ev.in);
+    float* bc = bcpart + ((long long)blk * a.M + t0 + last_tile) * 2 * a.N;   // the tile's dB, dC of this channel block
+    for (int tile = last_tile; tile >= 0; tile -= TT, ev = evn, bc -= 2 * TT * a.N) {
+        raw.template lay<false>(a, cb, t0 + tile, ev.in, s_dt, s_x, s_dy, s_B, s_C);
         __syncthreads();
 #pragma unroll 1
         for (int i0 = TT - kSub; i0 >= 0; i0 -= kSub) {
-            if (tile + i0 >= t1) continue;
+            if (tile + i0 >= nrow) continue;
             // the state in front of these rows: the checkpoint, and what reaches it of the segment's
             cp_async_wait();
             if (tile + i0 < reach) {
@@ -603,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                 const float2 v = *reinterpret_cast<const float2*>(slot(phase, k, m));
                 return F2{v.x, v.y};
             };
-            if (tile + i0 > t0) fetch(phase ^ 1);
+            if (tile + i0 > 0) fetch(phase ^ 1);
             float* red = s_red + (phase * kWarps + at.warp) * kSub * 2 * NP;
             auto rows = [&](auto evc) {
                 constexpr bool EV = decltype(evc)::value;
@@ -621,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                         const int r = i + j;
                         SeqRange sr{0, 0, 0, false};
                         const bool first = EV && (ev.first >> (i0 + r) & 1);
-                        if (first) sr = find_seq(a.cu, a.num_seqs, a.M, a.T, tile + i0 + r);
+                        if (first) sr = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + tile + i0 + r);
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             const F2 B = lds_pair(s_B + (i0 + r) * NP + at.n(m));
@@ -646,14 +631,16 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                         x4[k] = *reinterpret_cast<const float4*>(&s_x[cell<TT>(at.ch[k], i0 + i)]);
                         g4[k] = *reinterpret_cast<const float4*>(&s_dy[cell<TT>(at.ch[k], i0 + i)]);
                     }
-                    float pv[2][4], qv[2][4], yv[2][4];
+                    constexpr int KO = S == 1 ? 2 : 1;   // channels whose sums a lane ends with
+                    float pv[KO][4], qv[KO][4], yv[KO][4];
 #pragma unroll
                     for (int j = 3; j >= 0; --j) {
                         const int r = i + j;
                         const bool first = EV && (ev.first >> (i0 + r) & 1), last = EV && (ev.last >> (i0 + r) & 1);
                         SeqRange sr{0, 0, 0, false};
-                        if (first || last) sr = find_seq(a.cu, a.num_seqs, a.M, a.T, tile + i0 + r);
+                        if (first || last) sr = find_seq(a.cu, a.num_seqs, a.M, a.T, t0 + tile + i0 + r);
                         F2 B[2], C[2], dB[2], dC[2];
+                        float ps[2], qs[2], ys[2];
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
                             B[m] = lds_pair(s_B + (i0 + r) * NP + at.n(m));
@@ -685,19 +672,31 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
                                     dh[k][m] = F2{0.f, 0.f};
                                 }
                             }
-                            pv[k][j] = p.x + p.y;
-                            qv[k][j] = q.x + q.y;
-                            yv[k][j] = y.x + y.y;
+                            ps[k] = p.x + p.y;
+                            qs[k] = q.x + q.y;
+                            ys[k] = y.x + y.y;
+                        }
+                        if constexpr (S == 1) {
+#pragma unroll
+                            for (int k = 0; k < KO; ++k) {
+                                pv[k][j] = ps[k];
+                                qv[k][j] = qs[k];
+                                yv[k][j] = ys[k];
+                            }
+                        } else {
+                            pv[0][j] = channel_exchange<S>(ps[0], ps[1]);
+                            qv[0][j] = channel_exchange<S>(qs[0], qs[1]);
+                            yv[0][j] = channel_exchange<S>(ys[0], ys[1]);
                         }
                         channel_sum<S>(at, dB, dC, red + r * 2 * NP);
                     }
                     // p, q and y over the lanes; the lane that ends with a row (or two, or four) of a
                     // channel finishes it, in place of the row's dt, x and dy, which all lanes have read
-                    lane_sum42<S>(at, pv);
-                    lane_sum42<S>(at, qv);
-                    lane_sum42<S>(at, yv);
+                    row_exchange<S>(at, pv[0]);
+                    row_exchange<S>(at, qv[0]);
+                    row_exchange<S>(at, yv[0]);
 #pragma unroll
-                    for (int k = 0; k < (S == 1 ? 2 : 1); ++k) {
+                    for (int k = 0; k < KO; ++k) {
 #pragma unroll
                         for (int w = 0; w < (S >= 4 ? 1 : 2); ++w) {
                             const bool up = S >= 4 ? (at.s & 2) != 0 : w;
@@ -724,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
             __syncthreads();
             for (int k = tid; k < kSub * 2 * NP; k += kThreads) {
                 const int r = k / (2 * NP), w = k % (2 * NP) / NP, n = k % NP;
-                if (n >= a.N || tile + i0 + r >= a.M) continue;
+                if (n >= a.N || tile + i0 + r >= nrow) continue;
                 float t = 0.f;
 #pragma unroll
                 for (int x = 0; x < kWarps; ++x) t += s_red[(phase * kWarps + x) * kSub * 2 * NP + k];
@@ -743,16 +742,16 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
             pg[it] = raw.get(2, it);
             pz[it] = raw.get(3, it);   // without a z: nothing that is used
         }
-        if (tile > t0) {
-            evn = find_events(a, tile - TT, TT, seq);
-            raw.load(a, cb, tile - TT, evn.in);
+        if (tile > 0) {
+            evn = find_events(a, t0 + tile - TT, TT);
+            raw.load(a, cb, t0 + tile - TT, evn.in);
         }
 #pragma unroll
         for (int it = 0; it < NSLOT; ++it) {
             const int slot = it * kThreads + tid, row = slot / VPR, c0 = (slot % VPR) * 8;
             const int cn = max(0, min(8, cb.n - c0)), d = cb.d0 + c0;
             if (row >= TT || !(ev.in >> row & 1) || cn == 0) continue;
-            const long long t = tile + row;
+            const long long t = t0 + tile + row;
             float dx[8], v[8], z[8], g[8];
             unpack<T, 8>(pv[it], v);
             unpack<T, 8>(pg[it], g);
