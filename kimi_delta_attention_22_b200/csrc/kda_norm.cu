@@ -70,6 +70,17 @@ __device__ __forceinline__ long long div_by(long long a, int b) {   // a >= 0; 3
     return a <= 0xffffffffLL ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
+// Whether access c of a lane lies in the row.  The layouts (norm_t) give a row of vector accesses
+// more than half of the lanes' accesses, so only the upper half of them is ever compared; FULL:
+// the row fills all of them.  The comparisons cost more than they look: each keeps the access
+// apart as a branch of its own (65536 x 4096 gradient: 339 us with all, 294 us with none).
+template <int VEC, int L, int NC, bool FULL>
+__device__ __forceinline__ bool in_row(int c, int lane, int D) {
+    if constexpr (FULL) return true;
+    if (VEC > 1 && c < NC / 2) return true;
+    return (c * L + lane) * VEC < D;
+}
+
 // Parameters of an access' columns: fp32, at most 16 bytes at a time.
 template <int VEC>
 __device__ __forceinline__ void load_params(const float* p, float* o) {
@@ -80,7 +91,7 @@ __device__ __forceinline__ void load_params(const float* p, float* o) {
 template <int VEC>
 __device__ __forceinline__ F2 pair(const float* f, int v) { return F2{f[v], VEC > 1 ? f[VEC > 1 ? v + 1 : 0] : 0.f}; }
 
-template <typename T, int VEC, int L, int NC>
+template <typename T, int VEC, int L, int NC, bool FULL>
 __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a) {
     constexpr int NI = rows_per_item<L, NC>();
     __shared__ float2 buf[L > 32 ? 2 * (L / 32) : 1];
@@ -98,7 +109,7 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = (c * L + lane) * VEC;
-            px[r][c] = live && d < a.D ? load_pack<VEC>(xg + (row0 + r) * a.xs + d) : zero_pack<T, VEC>();
+            px[r][c] = live && in_row<VEC, L, NC, FULL>(c, lane, a.D) ? load_pack<VEC>(xg + (row0 + r) * a.xs + d) : zero_pack<T, VEC>();
         }
     }
     float w[NC][VEC], b[NC][VEC];
@@ -110,7 +121,7 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
             w[c][v] = 1.f;
             b[c][v] = 0.f;
         }
-        if (NI > 1 && d < a.D) {   // one row: read when they are needed instead
+        if (NI > 1 && in_row<VEC, L, NC, FULL>(c, lane, a.D)) {   // one row: read when they are needed instead
             if (a.w) load_params<VEC>(a.w + (long long)g * a.D + d, w[c]);
             if (a.b) load_params<VEC>(a.b + (long long)g * a.D + d, b[c]);
         }
@@ -129,7 +140,7 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
         F2 q{0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
-            if ((c * L + lane) * VEC < a.D) {
+            if (in_row<VEC, L, NC, FULL>(c, lane, a.D)) {
                 if constexpr (VEC == 1) {
                     f[c][0] -= mean;
                     q.x = fmaf(f[c][0], f[c][0], q.x);
@@ -151,7 +162,7 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = (c * L + lane) * VEC;
-            if (d >= a.D) continue;
+            if (!in_row<VEC, L, NC, FULL>(c, lane, a.D)) continue;
             if (NI == 1) {
                 if (a.w) load_params<VEC>(a.w + (long long)g * a.D + d, w[c]);
                 if (a.b) load_params<VEC>(a.b + (long long)g * a.D + d, b[c]);
@@ -175,6 +186,8 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
     }
 }
 
+constexpr int kStages = 3;   // rows in the ring, one of them being worked on
+
 // grid (K, G): CTA (k, g) walks rows k, k + K, .. (times the rows it holds at once) of group g.
 // RING: x and d_out of the next rows are copied ahead (STG - 1 rows) into slots of shared memory
 // that only the copying thread reads; without it the next row waits in registers.  A row is
@@ -187,11 +200,11 @@ constexpr int bwd_threads() {
     return NC * VEC <= 8 ? 1024 : NC == 2 && L > 32 && L <= 256 ? 768 : block_threads<L>() > 512 ? block_threads<L>() : 512;
 }
 
-template <typename T, int VEC, int L, int NC, bool RING>
+template <typename T, int VEC, int L, int NC, bool RING, bool FULL>
 __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() / block_threads<L>()) norm_bwd_kernel(NormArgs a, int K) {
-    constexpr int R = cta_rows<L>(), NT = block_threads<L>(), STG = 4;
+    constexpr int R = cta_rows<L>(), NT = block_threads<L>(), STG = kStages;
     __shared__ float2 buf[L > 32 ? 2 * (L / 32) : 1];
-    extern __shared__ __align__(16) uint4 ring[];   // [STG][2][NC][NT]
+    extern __shared__ __align__(16) uint4 ring[];   // [STG][2][NC][NT], then this thread's weights [NC][2][NT]
     int turn = 0;
     const int lane = threadIdx.x % L, sub = threadIdx.x / L;
     const int g = blockIdx.y;
@@ -202,19 +215,34 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
     T* og = static_cast<T*>(a.dx) + (long long)g * a.D + lane * VEC;
     const float* wg = a.w + (long long)g * a.D + lane * VEC;
     float dw[NC][VEC] = {}, db[NC][VEC] = {};
-    constexpr bool kKeep = NC * VEC <= 16;   // the weights fit in registers
-    float wk[kKeep ? NC : 1][VEC];
+    float4* s_w = reinterpret_cast<float4*>(ring + STG * 2 * NC * NT) + threadIdx.x;
     Pack<T, VEC> px[NC], pg[NC];
-    auto in = [&](int c) { return (c * L + lane) * VEC < a.D; };
+    auto in = [&](int c) { return in_row<VEC, L, NC, FULL>(c, lane, a.D); };
     auto weights = [&](int c, float* o) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) o[v] = 1.f;
         if (a.w != nullptr && in(c)) load_params<VEC>(wg + c * L * VEC, o);
     };
-    if constexpr (kKeep) {
+    if constexpr (RING) {
 #pragma unroll
-        for (int c = 0; c < NC; ++c) weights(c, wk[c]);
+        for (int c = 0; c < NC; ++c) {
+            float o[VEC];
+            weights(c, o);
+#pragma unroll
+            for (int v = 0; v < VEC; v += 4) s_w[(c * (VEC / 4) + v / 4) * NT] = make_float4(o[v], o[v + 1], o[v + 2], o[v + 3]);
+        }
     }
+    auto weights_again = [&](int c, float* o) {
+        if constexpr (RING) {
+#pragma unroll
+            for (int v = 0; v < VEC; v += 4) {
+                const float4 f = s_w[(c * (VEC / 4) + v / 4) * NT];
+                o[v] = f.x; o[v + 1] = f.y; o[v + 2] = f.z; o[v + 3] = f.w;
+            }
+        } else {
+            weights(c, o);
+        }
+    };
     // Every thread of the CTA makes the same number of turns (the sums meet in barriers).
     const long long first = (long long)blockIdx.x * R + sub;
     // running pointers: the row that is read (or copied ahead) next, the one that is written next
@@ -281,8 +309,8 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
             float x[VEC], y[VEC], wr[VEC];
             unpack<T, VEC>(px[c], x);
             unpack<T, VEC>(pg[c], y);
-            if constexpr (!kKeep) weights(c, wr);
-            const float* w = kKeep ? wk[kKeep ? c : 0] : wr;
+            weights_again(c, wr);
+            const float* w = wr;
 #pragma unroll
             for (int v = 0; v < VEC; v += (VEC > 1 ? 2 : 1)) {
                 const F2 xh = mul2(add2(pair<VEC>(x, v), both(-mu)), both(rs)), gy = pair<VEC>(y, v);
@@ -308,8 +336,8 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
                 float x[VEC], y[VEC], wr[VEC];
                 unpack<T, VEC>(px[c], x);
                 unpack<T, VEC>(pg[c], y);
-                if constexpr (!kKeep) weights(c, wr);
-                const float* w = kKeep ? wk[kKeep ? c : 0] : wr;
+                weights_again(c, wr);
+                const float* w = wr;
 #pragma unroll
                 for (int v = 0; v < VEC; v += (VEC > 1 ? 2 : 1)) {
                     const F2 gw = mul2(pair<VEC>(y, v), pair<VEC>(w, v));
@@ -395,15 +423,19 @@ cudaError_t fwd_one(const NormArgs& a, cudaStream_t s) {
     constexpr int NI = rows_per_item<L, NC>();
     const long long items = (a.rows + NI - 1) / NI * a.G, grid = (items + cta_rows<L>() - 1) / cta_rows<L>();
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    norm_fwd_kernel<T, VEC, L, NC><<<(unsigned)grid, block_threads<L>(), 0, s>>>(a);
+    const bool full = VEC > 1 && a.D == L * NC * VEC;
+    auto k = full ? norm_fwd_kernel<T, VEC, L, NC, (VEC > 1)> : norm_fwd_kernel<T, VEC, L, NC, false>;
+    k<<<(unsigned)grid, block_threads<L>(), 0, s>>>(a);
     return cudaGetLastError();
 }
 template <typename T, int VEC, int L, int NC>
 cudaError_t bwd_one(const NormArgs& a, cudaStream_t s) {
-    constexpr bool RING = VEC > 1 && NC * block_threads<L>() * 128 <= 200 * 1024;
-    constexpr int smem = RING ? NC * block_threads<L>() * 128 : 0;   // 4 rows' x and d_out
+    constexpr int bytes = NC * block_threads<L>() * (kStages * 32 + VEC * 4);
+    constexpr bool RING = VEC > 1 && bytes <= 200 * 1024;
+    constexpr int smem = RING ? bytes : 0;
     const int K = bwd_ctas(a.rows, a.G, cta_rows<L>(), block_threads<L>(), bwd_threads<VEC, L, NC>());
-    auto k = norm_bwd_kernel<T, VEC, L, NC, RING>;
+    const bool full = VEC > 1 && a.D == L * NC * VEC;
+    auto k = full ? norm_bwd_kernel<T, VEC, L, NC, RING, (VEC > 1)> : norm_bwd_kernel<T, VEC, L, NC, RING, false>;
     cudaError_t e;
     if (smem > 0 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
     k<<<dim3((unsigned)K, (unsigned)a.G), block_threads<L>(), smem, s>>>(a, K);
