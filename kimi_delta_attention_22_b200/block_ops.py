@@ -193,6 +193,14 @@ def _out(given, what, shape, dtype, device, like=None):
     return given, _want(given, what, shape, dtype, device)
 
 
+def _grads(given, names):
+    """The caller's gradient buffers by name."""
+    given = given or {}
+    if unknown := set(given) - set(names):
+        raise ValueError(f"unknown gradients {sorted(unknown)}: expected some of {names}")
+    return given
+
+
 def _check(st, name):
     if st != 0:
         raise _b.KDAError(st, name)
@@ -274,7 +282,7 @@ def kda_conv_bwd(x, weight, d_out, bias=None, state=None, d_final_state=None, cu
     dev = _cuda(x, "x")
     D, W, w, b, xs = _conv_common(x, weight, bias, dev, False)
     B, T, N = _batch(x, cu_seqlens, dev)
-    grads = grads or {}
+    grads = _grads(grads, ("dx", "dweight", "dbias", "dstate"))
     st = (N, max(W - 1, 0), D)
     sp = _want(state, "state", st, x.dtype, dev)
     dsp = _want(d_final_state, "d_final_state", st, x.dtype, dev)
@@ -385,7 +393,7 @@ def kda_ssm_bwd(x, dt, A, B, C, d_out, D=None, z=None, dt_bias=None, h0=None, d_
     dev = _cuda(x, "x")
     Dc, N, G, st, p = _ssm_common(x, dt, A, B, C, D, z, dt_bias, dev, False)
     b, T, n = _batch(x, cu_seqlens, dev)
-    grads = grads or {}
+    grads = _grads(grads, ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"))
     hp = _want(h0, "h0", (n, Dc, N), torch.float32, dev)
     dtp = _want(d_hT, "d_hT", (n, Dc, N), torch.float32, dev)
     dop = _want(d_out, "d_out", x.shape, x.dtype, dev)
@@ -468,7 +476,7 @@ def kda_layer_norm_bwd(d_out, x, mean, rstd, weight=None, want_params: bool = Tr
         G, inner, pshape = groups, 2, (groups, D)
         rows = x.numel() // (G * D) if G * D else 0
     xs = _strided(x, "x", x.shape, x.dtype, dev, inner, G * D)
-    grads = grads or {}
+    grads = _grads(grads, ("dx", "dweight", "dbias"))
     dp = _want(d_out, "d_out", x.shape, x.dtype, dev)
     mp = _want(mean, "mean", x.shape[:-1], torch.float32, dev)
     rp = _want(rstd, "rstd", x.shape[:-1], torch.float32, dev)

@@ -132,6 +132,7 @@ kda_status_t kda_conv_fwd(const kda_conv_shape_t* sh, const void* x, const float
     if (!aligned(x, el) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(state0, el) || !aligned(cu_seqlens, 4) ||
         !aligned(out, el) || !aligned(stateT, el))
         return KDA_ERR_MISALIGNED;
+    if (a.M > 0 && out == x) return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return status_of(kda::launch_conv_fwd(a, sh->dtype == KDA_BF16, sh->activation == 1, static_cast<cudaStream_t>(stream)));
 }
@@ -175,6 +176,7 @@ kda_status_t kda_conv_bwd(const kda_conv_shape_t* sh, const void* x, const float
     const size_t need = kda_conv_bwd_workspace_size(sh);
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
+    if (a.M > 0 && (dx == x || dx == d_out)) return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.part = reinterpret_cast<float*>(ws);
         return kda::launch_conv_bwd(a, sh->dtype == KDA_BF16, sh->grad_dtype == KDA_BF16, sh->activation == 1,
@@ -202,6 +204,7 @@ kda_status_t kda_ssm_fwd(const kda_ssm_shape_t* sh, const void* x, const void* d
     const size_t need = kda_ssm_fwd_workspace_size(sh, cu_seqlens != nullptr);
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
+    if (a.M > 0 && (out == x || out == delta || out == z)) return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.ws = ws;
@@ -253,6 +256,11 @@ kda_status_t kda_ssm_bwd(const kda_ssm_shape_t* sh, const void* x, const void* d
     const size_t need = kda_ssm_bwd_workspace_size(sh, cu_seqlens != nullptr);
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
+    const void* const in[] = {x, delta, z, Bm, Cm, d_out};
+    const void* const grads[] = {dx, ddelta, dz, dB, dC};
+    for (const void* g : grads)
+        for (const void* i : in)
+            if (a.M > 0 && g != nullptr && g == i) return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.ws = ws;
         return kda::launch_ssm_bwd(a, sh->dtype == KDA_BF16, static_cast<cudaStream_t>(stream));

@@ -13,14 +13,14 @@
 //   1. summary: every segment alone, scanned once from zero, gives its last state, the
 //      gradient that its rows send to the state in front of it (sum_t (prod a) C dy, the
 //      running product taken along, so no second exponential), the sum of dt, and both
-//      states and sums in front of every 8 rows (checkpoints).
+//      states and sums in front of every 4 rows (checkpoints).
 //   2. join: along the segments, forward for the incoming states, backward for the
 //      incoming state gradients (the decay over a segment is e^{A sum dt}).
-//   3. gradients, all segments in parallel, each from its last 8 rows back: the checkpoint
-//      plus the decayed incoming state, then the 8 rows' states and decays into registers,
-//      then the 8 rows in reverse.
+//   3. gradients, all segments in parallel, each from its last 4 rows back: the checkpoint
+//      plus the decayed incoming state, then the 4 rows' states and decays into registers,
+//      then the 4 rows in reverse.
 //   4. sums: of dB and dC over the channel blocks, of dA, dDskip and the bias over segments.
-// Two sets of exponentials (and one in 8 rows for the checkpoints) and about 18 fp32
+// Two sets of exponentials (and one in 4 rows for the checkpoints) and about 18 fp32
 // operations per row, channel and state: the special-function, fp32 and shared-memory
 // pipes are all near their limits at once; the bytes take a fifth of the time.
 //
@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
     const long long t0 = sg * seg.len, t1 = t0 + seg.len < a.M ? t0 + seg.len : a.M;
     F2 A2[2][2], h[2][2], p[2][2], g[2][2];
     float dtsum[2] = {0.f, 0.f};
+    bool open = true;   // the first row's sequence goes on: what follows it must not touch g (0 * NaN)
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -328,8 +329,9 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
             }
             ck += a.D * NP;
             dk += a.D;
-            auto rows = [&](auto evc) {   // eight rows, with or without sequences that begin or end there
-                constexpr bool EV = decltype(evc)::value;
+            // four rows, with or without sequences that begin or end there
+            auto rows = [&](auto evc, auto goes_on) {
+                constexpr bool EV = decltype(evc)::value, OPEN = decltype(goes_on)::value;
 #pragma unroll
                 for (int i = i0; i < i0 + kSub; i += 4) {
                     float4 d4[2], u4[2], g4[2];
@@ -348,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
 #pragma unroll
                                 for (int m = 0; m < 2; ++m) {
                                     h[k][m] = at.get(a.h0, r.q, a, k, m);
-                                    if (tile + i + j > t0) p[k][m] = F2{0.f, 0.f};   // behind the first sequence's end
                                 }
+                            if (tile + i + j > t0) open = false;
                         }
 #pragma unroll
                         for (int m = 0; m < 2; ++m) {
@@ -361,26 +363,29 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
                                 const float dy = j == 0 ? g4[k].x : j == 1 ? g4[k].y : j == 2 ? g4[k].z : g4[k].w;
                                 const F2 e = ex2(mul2(both(dt), A2[k][m]));
                                 h[k][m] = fma2(e, h[k][m], mul2(both(u), B));
-                                p[k][m] = mul2(p[k][m], e);
-                                g[k][m] = fma2(p[k][m], mul2(both(dy), C), g[k][m]);
+                                if (EV ? open : OPEN) {
+                                    p[k][m] = mul2(p[k][m], e);
+                                    g[k][m] = fma2(p[k][m], mul2(both(dy), C), g[k][m]);
+                                }
                                 if (m == 0) dtsum[k] += dt;
                             }
                         }
-                        if (EV && (ev.last >> (i + j) & 1)) {
+                        if (EV && open && (ev.last >> (i + j) & 1)) {
                             const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, tile + i + j);
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
 #pragma unroll
                                 for (int m = 0; m < 2; ++m) {
                                     g[k][m] = fma2(p[k][m], at.get(a.d_hT, r.q, a, k, m), g[k][m]);
-                                    p[k][m] = F2{0.f, 0.f};
                                 }
+                            open = false;
                         }
                     }
                 }
             };
-            if ((ev.first | ev.last) >> i0 & ((1u << kSub) - 1)) rows(std::true_type{});
-            else rows(std::false_type{});
+            if ((ev.first | ev.last) >> i0 & ((1u << kSub) - 1)) rows(std::true_type{}, std::true_type{});
+            else if (open) rows(std::false_type{}, std::true_type{});
+            else rows(std::false_type{}, std::false_type{});
         }
     }
 #pragma unroll
@@ -500,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
     constexpr int CH = channels<S>(), TT = tile_rows<S>(), NP = 4 * S, VPR = CH / 8;
     extern __shared__ __align__(16) float sm[];
     Raw<T, S, ALIGNED> raw(sm);
-    // dt, x and dy of the tile; eight rows on, dx, ddelta (without softplus' slope) and y in their place
+    // dt, x and dy of the tile; as rows are finished, dx, ddelta (without
+    // softplus' slope) and y in their place
     float *s_dt = sm + Raw<T, S, ALIGNED>::kBytes / 4, *s_x = s_dt + CH * TT, *s_dy = s_x + CH * TT, *s_red = s_dy + CH * TT;
     float* s_ck = s_red + 2 * kWarps * kSub * 2 * NP;   // two checkpoints, then the segment's incoming state
     T *s_B = reinterpret_cast<T*>(s_ck + 3 * kCk + 8 * kThreads), *s_C = s_B + TT * NP;

@@ -168,6 +168,34 @@ def test_special_values_stay_in_their_window():
 
 
 @pytest.mark.gpu
+def test_bad_values_stay_in_their_sequence():
+    """A NaN sequence, and NaN rows of no sequence, leave the others as they were, bit for bit."""
+    lens = [40, 3, 70, 1, 90]
+    cu = lengths(lens)
+    d = draw(1, cu[-1] + 7, 24, 4, BF, cu, seed=31)
+    o = dev(d)
+    y, fin = kda.kda_conv_fwd(o["x"], o["w"], o["bias"], o["state"], o["cu"])
+    g = kda.kda_conv_bwd(o["x"], o["w"], o["dy"], o["bias"], o["state"], o["dfin"], o["cu"])
+    for bad in range(5):
+        p = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in o.items()}
+        for k in ("x", "dy"):
+            p[k][:, cu[bad]:cu[bad + 1]] = float("nan")
+            p[k][:, cu[-1]:] = float("nan")
+        p["state"][bad] = p["dfin"][bad] = float("nan")
+        y2, fin2 = kda.kda_conv_fwd(p["x"], p["w"], p["bias"], p["state"], p["cu"])
+        g2 = kda.kda_conv_bwd(p["x"], p["w"], p["dy"], p["bias"], p["state"], p["dfin"], p["cu"])
+        keep = [n for n in range(5) if n != bad]
+        rows = torch.cat([torch.arange(cu[n], cu[n + 1]) for n in keep]).cuda()
+        assert torch.equal(y2[:, rows], y[:, rows]) and torch.equal(fin2[keep], fin[keep])
+        assert torch.equal(g2["dx"][:, rows], g["dx"][:, rows]) and torch.equal(g2["dstate"][keep], g["dstate"][keep])
+    p = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in o.items()}
+    for k in ("x", "dy"):
+        p[k][:, cu[-1]:] = float("nan")
+    g2 = kda.kda_conv_bwd(p["x"], p["w"], p["dy"], p["bias"], p["state"], p["dfin"], p["cu"])
+    assert torch.equal(g2["dweight"], g["dweight"]) and torch.equal(g2["dbias"], g["dbias"])
+
+
+@pytest.mark.gpu
 def test_inconsistent_cu_seqlens_is_flagged():
     """A broken bound sets the status word; consistent neighbours keep their rows; no row of
     another sequence is written."""
@@ -207,6 +235,10 @@ def test_binding_refusals():
         kda.kda_conv_fwd(x, torch.zeros(16, 9, device="cuda"))
     with pytest.raises(kda.KDAError):
         kda.kda_conv_fwd(x, w, state=o["state"], final_state=o["state"])
+    with pytest.raises(kda.KDAError):
+        kda.kda_conv_fwd(x, w, out=x)
+    with pytest.raises(ValueError):
+        kda.kda_conv_bwd(x, w, o["dy"], grads=dict(dw=w))
     with pytest.raises(TypeError):
         kda.kda_conv_bwd(x.float(), w, o["dy"])                  # bf16 gradient of an fp32 input
 

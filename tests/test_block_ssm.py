@@ -267,6 +267,42 @@ def test_inconsistent_cu_seqlens_is_flagged():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("lens", [[90, 70, 200, 33], [400, 300, 500, 70], [3, 2, 5, 4]])
+def test_bad_values_stay_in_their_sequence(lens):
+    """NaN and infinities in one sequence's rows, states and state gradients leave every other
+    sequence's outputs and gradients as they were, bit for bit; the same in rows of no sequence."""
+    cu = lengths(lens)
+    T = cu[-1] + 9
+    d = draw(1, T, 24, 16, 2, F32, cu, seed=21)
+    o = dev(d)
+    good, hT = forward(o)
+    gg = backward(o)
+    for bad in (1, 2):
+        b, e = cu[bad], cu[bad + 1]
+        for value in (float("nan"), float("inf")):
+            p = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in o.items()}
+            for k in ("x", "dt", "B", "C", "z", "dy"):
+                p[k][:, b:e] = value
+                p[k][:, cu[-1]:] = value
+            p["h0"][bad] = value
+            p["dh"][bad] = value
+            out, h = forward(p)
+            g = backward(p)
+            keep = [n for n in range(len(lens)) if n != bad]
+            rows = torch.cat([torch.arange(cu[n], cu[n + 1]) for n in keep]).cuda()
+            assert torch.equal(out[:, rows], good[:, rows]) and torch.equal(h[keep], hT[keep])
+            for k in ("dx", "ddt", "dz", "dB", "dC"):
+                assert torch.equal(g[k][:, rows], gg[k][:, rows]), (bad, value, k)
+            assert torch.equal(g["dh0"][keep], gg["dh0"][keep])
+    p = {k: (v.clone() if isinstance(v, torch.Tensor) else v) for k, v in o.items()}
+    for k in ("x", "dt", "B", "C", "z", "dy"):
+        p[k][:, cu[-1]:] = float("nan")
+    g = backward(p)
+    for k in ("dA", "dD", "ddt_bias", "dh0"):
+        assert torch.equal(g[k], gg[k]), k
+
+
+@pytest.mark.gpu
 def test_binding_refusals():
     o = dev(draw(2, 8, 16, 16, 1, BF, seed=1))
     args = [o[k] for k in ("x", "dt", "A", "B", "C")]
@@ -292,6 +328,12 @@ def test_binding_refusals():
         call(D=o["D"].cpu())
     with pytest.raises(kda.KDAError):
         call(h0=o["h0"], hT=o["h0"])
+    with pytest.raises(kda.KDAError):
+        call(out=o["x"])
+    with pytest.raises(ValueError):
+        kda.kda_ssm_bwd(*args, o["dy"], grads=dict(dX=o["dy"].clone()))
+    with pytest.raises(kda.KDAError):
+        kda.kda_ssm_bwd(*args, o["dy"], grads=dict(dx=o["dy"]))
     with pytest.raises(kda.KDAError):
         kda.kda_ssm_fwd(o["x"], o["dt"], torch.zeros(16, 129, device="cuda"), torch.zeros(2, 8, 129, dtype=BF, device="cuda"),
                         torch.zeros(2, 8, 129, dtype=BF, device="cuda"))
