@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 
 import torch
 
@@ -39,6 +40,13 @@ class NormShape(ctypes.Structure):
     """kda_norm_shape_t"""
     _fields_ = [("rows", _i64), ("groups", _i32), ("D", _i32), ("dtype", _i32), ("eps", ctypes.c_float),
                 ("x_stride", _i64)]
+
+
+@functools.lru_cache(maxsize=1024)
+def _shape(cls, *fields):
+    """A shape structure by reference.  The library only reads it, so calls of the same sizes share
+    one: building it takes a good part of the host's time of a small call."""
+    return ctypes.byref(cls(*fields))
 
 
 def declare(lib) -> None:
@@ -241,10 +249,10 @@ def kda_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, silu: bool =
     fp = None
     if final_state is not None or want_state:
         final_state, fp = _out(final_state, "final_state", st, x.dtype, dev)
-    sh = ConvShape(B, T, D, N, W, _code(x, "x"), 0, int(bool(silu)), xs, _status_ptr(dev_status, dev))
+    sh = _shape(ConvShape, B, T, D, N, W, _code(x, "x"), 0, int(bool(silu)), xs, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
-        _check(lib.kda_conv_fwd(ctypes.byref(sh), x.data_ptr(), w, b, sp, _ptr(cu_seqlens), op, fp, _stream(dev)),
+        _check(lib.kda_conv_fwd(sh, x.data_ptr(), w, b, sp, _ptr(cu_seqlens), op, fp, _stream(dev)),
                "kda_conv_fwd")
     return out, final_state
 
@@ -261,10 +269,10 @@ def kda_conv_step(x, weight, state, bias=None, silu: bool = True, out=None, lib=
         raise ValueError("state is required")
     sp = _want(state, "state", (N, max(W - 1, 0), D), x.dtype, dev)
     out, op = _out(out, "out", x.shape, x.dtype, dev, x)
-    sh = ConvShape(N, 1, D, N, W, _code(x, "x"), 0, int(bool(silu)), xs, None)
+    sh = _shape(ConvShape, N, 1, D, N, W, _code(x, "x"), 0, int(bool(silu)), xs, None)
     lib = lib or _b.load_library()
     with _on(dev):
-        _check(lib.kda_conv_step(ctypes.byref(sh), x.data_ptr(), w, b, sp, op, _stream(dev)), "kda_conv_step")
+        _check(lib.kda_conv_step(sh, x.data_ptr(), w, b, sp, op, _stream(dev)), "kda_conv_step")
     return out
 
 
@@ -296,11 +304,11 @@ def kda_conv_bwd(x, weight, d_out, bias=None, state=None, d_final_state=None, cu
         db, dbp = _out(grads.get("dbias"), "dbias", (D,), torch.float32, dev)
     if want_dstate:
         dst, dstp = _out(grads.get("dstate"), "dstate", st, x.dtype, dev)
-    sh = ConvShape(B, T, D, N, W, _code(x, "x"), _code(d_out, "d_out"), int(bool(silu)), xs, _status_ptr(dev_status, dev))
+    sh = _shape(ConvShape, B, T, D, N, W, _code(x, "x"), _code(d_out, "d_out"), int(bool(silu)), xs, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
-        ws, wp, wn = _workspace(workspace, lib.kda_conv_bwd_workspace_size(ctypes.byref(sh)) if workspace is True else 0, dev)
-        _check(lib.kda_conv_bwd(ctypes.byref(sh), x.data_ptr(), w, b, sp, _ptr(cu_seqlens), dp, dsp, dxp, dwp, dbp, dstp,
+        ws, wp, wn = _workspace(workspace, lib.kda_conv_bwd_workspace_size(sh) if workspace is True else 0, dev)
+        _check(lib.kda_conv_bwd(sh, x.data_ptr(), w, b, sp, _ptr(cu_seqlens), dp, dsp, dxp, dwp, dbp, dstp,
                                 wp, wn, _stream(dev)), "kda_conv_bwd")
     return dict(dx=dx, dweight=dw, dbias=db, dstate=dst)
 
@@ -352,12 +360,12 @@ def kda_ssm_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlen
     tp = None
     if hT is not None or want_state:
         hT, tp = _out(hT, "hT", (n, Dc, N), torch.float32, dev)
-    sh = SsmShape(b, T, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, _status_ptr(dev_status, dev))
+    sh = _shape(SsmShape, b, T, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
-        need = lib.kda_ssm_fwd_workspace_size(ctypes.byref(sh), int(cu_seqlens is not None)) if workspace is True else 0
+        need = lib.kda_ssm_fwd_workspace_size(sh, int(cu_seqlens is not None)) if workspace is True else 0
         ws, wp, wn = _workspace(workspace, need, dev)
-        _check(lib.kda_ssm_fwd(ctypes.byref(sh), *p, hp, _ptr(cu_seqlens), op, tp, wp, wn, _stream(dev)), "kda_ssm_fwd")
+        _check(lib.kda_ssm_fwd(sh, *p, hp, _ptr(cu_seqlens), op, tp, wp, wn, _stream(dev)), "kda_ssm_fwd")
     return out, hT
 
 
@@ -373,10 +381,10 @@ def kda_ssm_step(x, dt, A, B, C, h, D=None, z=None, dt_bias=None, softplus: bool
         raise ValueError("h is required")
     hp = _want(h, "h", (n, Dc, N), torch.float32, dev)
     out, op = _out(out, "out", x.shape, x.dtype, dev, x)
-    sh = SsmShape(n, 1, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, None)
+    sh = _shape(SsmShape, n, 1, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, None)
     lib = lib or _b.load_library()
     with _on(dev):
-        _check(lib.kda_ssm_step(ctypes.byref(sh), *p, hp, op, _stream(dev)), "kda_ssm_step")
+        _check(lib.kda_ssm_step(sh, *p, hp, op, _stream(dev)), "kda_ssm_step")
     return out
 
 
@@ -404,12 +412,12 @@ def kda_ssm_bwd(x, dt, A, B, C, d_out, D=None, z=None, dt_bias=None, h0=None, d_
                                    ("dz", x.shape, like, z is not None), ("ddt_bias", (Dc,), f32, dt_bias is not None),
                                    ("dh0", (n, Dc, N), f32, want_dh0)):
         r[name], q[name] = _out(grads.get(name), name, shape, dtype, dev) if on else (None, None)
-    sh = SsmShape(b, T, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, _status_ptr(dev_status, dev))
+    sh = _shape(SsmShape, b, T, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
-        need = lib.kda_ssm_bwd_workspace_size(ctypes.byref(sh), int(cu_seqlens is not None)) if workspace is True else 0
+        need = lib.kda_ssm_bwd_workspace_size(sh, int(cu_seqlens is not None)) if workspace is True else 0
         ws, wp, wn = _workspace(workspace, need, dev)
-        _check(lib.kda_ssm_bwd(ctypes.byref(sh), *p, hp, _ptr(cu_seqlens), dop, dtp, q["dx"], q["ddt"], q["dA"], q["dB"],
+        _check(lib.kda_ssm_bwd(sh, *p, hp, _ptr(cu_seqlens), dop, dtp, q["dx"], q["ddt"], q["dA"], q["dB"],
                                q["dC"], q["dD"], q["dz"], q["ddt_bias"], q["dh0"], wp, wn, _stream(dev)), "kda_ssm_bwd")
     return r
 
@@ -449,12 +457,12 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, w
     out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     mean = rstd = mp = rp = None
     if want_stats:
-        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev)
+        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
-    sh = NormShape(rows, G, D, _code(x, "x"), float(eps), xs)
+    sh = _shape(NormShape, rows, G, D, _code(x, "x"), float(eps), xs)
     lib = lib or _b.load_library()
     with _on(dev):
-        _check(lib.kda_layer_norm_fwd(ctypes.byref(sh), x.data_ptr(), w, b, op, mp, rp, _stream(dev)), "kda_layer_norm_fwd")
+        _check(lib.kda_layer_norm_fwd(sh, x.data_ptr(), w, b, op, mp, rp, _stream(dev)), "kda_layer_norm_fwd")
     return out, mean, rstd
 
 
@@ -485,11 +493,11 @@ def kda_layer_norm_bwd(d_out, x, mean, rstd, weight=None, want_params: bool = Tr
     if want_params:
         dw, dwp = _out(grads.get("dweight"), "dweight", pshape, torch.float32, dev)
         db, dbp = _out(grads.get("dbias"), "dbias", pshape, torch.float32, dev)
-    sh = NormShape(rows, G, D, _code(x, "x"), 0.0, xs)
+    sh = _shape(NormShape, rows, G, D, _code(x, "x"), 0.0, xs)
     lib = lib or _b.load_library()
     with _on(dev):
-        need = lib.kda_layer_norm_bwd_workspace_size(ctypes.byref(sh)) if workspace is True and want_params else 0
+        need = lib.kda_layer_norm_bwd_workspace_size(sh) if workspace is True and want_params else 0
         ws, wp, wn = _workspace(workspace, need, dev)
-        _check(lib.kda_layer_norm_bwd(ctypes.byref(sh), dp, x.data_ptr(), w, mp, rp, dxp, dwp, dbp, wp, wn, _stream(dev)),
+        _check(lib.kda_layer_norm_bwd(sh, dp, x.data_ptr(), w, mp, rp, dxp, dwp, dbp, wp, wn, _stream(dev)),
                "kda_layer_norm_bwd")
     return dict(dx=dx, dweight=dw, dbias=db)

@@ -349,6 +349,13 @@ __device__ __forceinline__ Pack<T, VEC> lds_pack(const void* p) {
     return r;
 }
 
+// Dynamic shared memory beyond the 48 KB that a kernel may use unasked.
+template <typename K>
+inline cudaError_t allow_smem(K k, size_t bytes) {
+    if (bytes <= 48 * 1024) return cudaSuccess;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 // Whether every access of VEC * el bytes at p + k * stride_bytes is aligned.
 inline bool vec_ok(const void* p, long long stride_bytes, int bytes) {
     return p == nullptr || ((reinterpret_cast<uintptr_t>(p) % (unsigned)bytes) == 0 && stride_bytes % bytes == 0);

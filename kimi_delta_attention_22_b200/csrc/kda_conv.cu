@@ -168,35 +168,53 @@ __global__ void __launch_bounds__(256, WM <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs
     }
 }
 
+// One row: a thread takes its channels of kSeqs sequences, whose loads are under way together and
+// share one read of the taps (64 bytes per thread, as much as a sequence's state and input).
+constexpr int kSeqs = 4;
+
 template <typename T, int VEC, int WM, bool SILU>
 __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
     const int nvec = a.D / VEC;
     const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-    const long long n = idx / nvec, d0 = (idx % nvec) * VEC;
-    if (n >= a.num_seqs) return;
-    T* st = static_cast<T*>(a.stateT) + n * (a.W - 1) * a.D + d0;
-    Pack<T, VEC> win[WM - 1];
+    const long long n0 = idx / nvec * kSeqs, d0 = (idx % nvec) * VEC;
+    if (n0 >= a.num_seqs) return;
+    const long long ss = (long long)(a.W - 1) * a.D;   // a sequence's state
+    T* st = static_cast<T*>(a.stateT) + n0 * ss + d0;
+    const T* x = static_cast<const T*>(a.x) + n0 * a.xs + d0;
+    T* out = static_cast<T*>(a.out) + n0 * a.D + d0;
+    Pack<T, VEC> win[kSeqs][WM];
 #pragma unroll
-    for (int j = 0; j < WM - 1; ++j) {
-        const int k = j - (WM - a.W);
-        win[j] = zero_pack<T, VEC>();
-        if (k >= 0) win[j] = load_pack<VEC>(st + (long long)k * a.D);
+    for (int q = 0; q < kSeqs; ++q) {
+        const bool on = n0 + q < a.num_seqs;
+#pragma unroll
+        for (int j = 0; j < WM - 1; ++j) {
+            const int k = j - (WM - a.W);
+            win[q][j] = on && k >= 0 ? load_pack<VEC>(st + q * ss + (long long)k * a.D) : zero_pack<T, VEC>();
+        }
+        win[q][WM - 1] = on ? load_pack<VEC>(x + q * a.xs) : zero_pack<T, VEC>();
     }
-    const Pack<T, VEC> cur = load_pack<VEC>(static_cast<const T*>(a.x) + n * a.xs + d0);
-    float wr[WM][VEC], br[VEC], pre[VEC], fw[WM - 1][VEC], fc[VEC];
+    float wr[WM][VEC], br[VEC];
     load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
 #pragma unroll
-    for (int j = 0; j < WM - 1; ++j) unpack<T, VEC>(win[j], fw[j]);
-    unpack<T, VEC>(cur, fc);
-    conv_pre<VEC, WM>(fw, fc, wr, br, pre);
-    if (SILU) silu_n<VEC, sizeof(T) == 2>(pre);
-    store_f32<T, VEC>(static_cast<T*>(a.out) + n * a.D + d0, pre);
+    for (int q = 0; q < kSeqs; ++q) {
+        if (n0 + q >= a.num_seqs) break;
+        float pre[VEC];
 #pragma unroll
-    for (int j = 1; j < WM - 1; ++j) {
-        const int k = j - 1 - (WM - a.W);
-        if (k >= 0) store_pack<T, VEC>(st + (long long)k * a.D, win[j]);
+        for (int v = 0; v < VEC; ++v) pre[v] = br[v];
+#pragma unroll
+        for (int j = 0; j < WM; ++j) {
+            float f[VEC];
+            unpack<T, VEC>(win[q][j], f);
+            fma_n<VEC>(wr[j], f, pre);
+        }
+        if (SILU) silu_n<VEC, sizeof(T) == 2>(pre);
+        store_f32<T, VEC>(out + q * a.D, pre);
+#pragma unroll
+        for (int j = 1; j < WM; ++j) {   // the state moves up by one row
+            const int k = j - 1 - (WM - a.W);
+            if (k >= 0) store_pack<T, VEC>(st + q * ss + (long long)k * a.D, win[q][j]);
+        }
     }
-    store_pack<T, VEC>(st + (long long)(a.W - 2) * a.D, cur);
 }
 
 // Backward.  A CTA owns 32 * VEC channels; its eight warps walk runs of rows and keep
@@ -432,13 +450,13 @@ cudaError_t fwd_w(const ConvArgs& a, cudaStream_t s) {
              : a.W == 4 ? conv_fwd_kernel<T, VEC, 4, SILU>
                         : conv_fwd_kernel<T, VEC, 8, SILU>;
     cudaError_t e;
-    if (smem > 0 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
     k<<<(unsigned)grid, 256, smem, s>>>(a, run, nruns);
     return cudaGetLastError();
 }
 template <typename T, int VEC, bool SILU>
 cudaError_t step_w(const ConvArgs& a, cudaStream_t s) {
-    const long long grid = ((long long)(a.D / VEC) * a.num_seqs + 255) / 256;
+    const long long grid = ((long long)(a.D / VEC) * ((a.num_seqs + kSeqs - 1) / kSeqs) + 255) / 256;
     if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     switch (a.W) {
         case 2: conv_step_kernel<T, VEC, 2, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
@@ -456,7 +474,7 @@ cudaError_t bwd_one(const ConvArgs& a, cudaStream_t s) {
     constexpr int ring = VEC > 1 ? kBwdAhead * kU * 32 * kBwdWarps * VEC * (int)(sizeof(T) + sizeof(TG)) : 0;
     constexpr int smem = sums > ring ? sums : ring;
     auto k = conv_bwd_kernel<T, TG, VEC, WM, SILU>;
-    cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = allow_smem(k, smem);
     if (e != cudaSuccess) return e;
     k<<<grid, 32 * kBwdWarps, smem, s>>>(a, p.run, p.nruns, p.K);
     e = cudaGetLastError();
@@ -477,8 +495,7 @@ cudaError_t bwd_act(const ConvArgs& a, bool silu, cudaStream_t s) {
     return silu ? bwd_w<T, TG, VEC, true>(a, s) : bwd_w<T, TG, VEC, false>(a, s);
 }
 
-// 16-byte (forward, step) or 8-byte (bf16 backward) accesses need every row of every
-// tensor to start on such a boundary.
+// Accesses of `vec` elements need every row of every tensor to start on such a boundary.
 bool rows_ok(const ConvArgs& a, int el, int vec) {
     const int by = el * vec;
     const long long row = (long long)a.D * el;
@@ -497,7 +514,7 @@ cudaError_t fwd_t(const ConvArgs& a, bool silu, cudaStream_t s) {
 }
 template <typename T>
 cudaError_t step_t(const ConvArgs& a, bool silu, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
+    constexpr int V = 4;
     if (rows_ok(a, sizeof(T), V)) return silu ? step_w<T, V, true>(a, s) : step_w<T, V, false>(a, s);
     return silu ? step_w<T, 1, true>(a, s) : step_w<T, 1, false>(a, s);
 }

@@ -437,7 +437,7 @@ cudaError_t bwd_one(const NormArgs& a, cudaStream_t s) {
     const bool full = VEC > 1 && a.D == L * NC * VEC;
     auto k = full ? norm_bwd_kernel<T, VEC, L, NC, RING, (VEC > 1)> : norm_bwd_kernel<T, VEC, L, NC, RING, false>;
     cudaError_t e;
-    if (smem > 0 && (e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
     k<<<dim3((unsigned)K, (unsigned)a.G), block_threads<L>(), smem, s>>>(a, K);
     e = cudaGetLastError();
     if (e != cudaSuccess || a.part == nullptr) return e;
@@ -464,7 +464,7 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
     if (norm_vec(a, sizeof(T))) {
         const int n = a.D / V;   // accesses per row
         if (n <= 8) KDA_NORM(V, 8, 1);
-        if (n <= 16) KDA_NORM(V, 16, 1);
+        if (n <= 16) KDA_NORM(V, 8, 2);
         if (n <= 32) KDA_NORM(V, 32, 1);
         if (n <= 64) KDA_NORM(V, 32, 2);
         if constexpr (BWD) {   // longer runs per lane: the row's sums and copies cost the same for each lane

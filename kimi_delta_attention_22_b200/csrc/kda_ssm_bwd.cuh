@@ -887,7 +887,7 @@ cudaError_t go(const SsmArgs& a, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     if (K + extra > 0) {
         auto k1 = ssm_bwd_summary_kernel<T, S, ALIGNED>;
-        if ((e = cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm1)) != cudaSuccess) return e;
+        if ((e = allow_smem(k1, sm1)) != cudaSuccess) return e;
         k1<<<(unsigned)(l.nblk * (K + extra)), kThreads, sm1, s>>>(a, l.seg, l.nblk, hseg, rseg, dtseg, hck, dtck, flags);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
     }
@@ -895,7 +895,7 @@ cudaError_t go(const SsmArgs& a, cudaStream_t s) {
         ssm_bwd_join_kernel<<<dim3((unsigned)((dnp + 127) / 128), 2), 128, 0, s>>>(a, 4 * S, K, hseg, rseg, dtseg, flags);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         auto k3 = ssm_bwd_grad_kernel<T, S, ALIGNED>;
-        if ((e = cudaFuncSetAttribute(k3, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sm3)) != cudaSuccess) return e;
+        if ((e = allow_smem(k3, sm3)) != cudaSuccess) return e;
         k3<<<(unsigned)(l.nblk * K), kThreads, sm3, s>>>(a, l.seg, l.nblk, hseg, rseg, hck, dtck, part, bcpart);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         ssm_bwd_bc_kernel<T><<<(unsigned)((bc + 255) / 256), 256, 0, s>>>(a, l.per, bcpart);

@@ -395,7 +395,7 @@ cudaError_t fwd_go(const SsmArgs& a, const Segments& p, cudaStream_t s) {
     if (!p.whole) {
         auto k = ssm_scan_kernel<T, S, NS, ALIGNED, true>;
         constexpr int sm1 = scan_smem<T, S, NS, true>();
-        if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm1)) != cudaSuccess) return e;
+        if ((e = allow_smem(k, sm1)) != cudaSuccess) return e;
         k<<<(unsigned)(blocks * p.count), 2 * kThreads, sm1, s>>>(a, p, nblk, hseg, dtseg);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         const long long dn = (long long)a.D * a.N;
@@ -404,7 +404,7 @@ cudaError_t fwd_go(const SsmArgs& a, const Segments& p, cudaStream_t s) {
     }
     auto k = ssm_scan_kernel<T, S, NS, ALIGNED, false>;
     constexpr int sm2 = scan_smem<T, S, NS, false>();
-    if ((e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, sm2)) != cudaSuccess) return e;
+    if ((e = allow_smem(k, sm2)) != cudaSuccess) return e;
     k<<<(unsigned)(blocks * (p.count + extra)), 2 * kThreads, sm2, s>>>(a, p, nblk, hseg, dtseg);
     return cudaGetLastError();
 }
