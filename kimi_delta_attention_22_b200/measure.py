@@ -4,6 +4,7 @@
                                                    [--iters 10] [--warmup 3] [--shape B,T,H]
     python -m kimi_delta_attention_22_b200.measure --recurrent [--tokens 1,4,16,64]
     python -m kimi_delta_attention_22_b200.measure --chunk-backward workload[,workload...]
+    python -m kimi_delta_attention_22_b200.measure --block [--block-shape B,T,D,N]
 
 For each workload: inputs drawn once on the device (kimi_delta_attention_22_b200.inputs),
 the prefill's workspace allocated once (--schedule pool: none, so each call takes its
@@ -19,6 +20,11 @@ One JSON line per workload.
 32 heads, d = 128, bf16, per-channel gates) for each token count T, next to T calls
 of kda_decode_step on the same inputs, with the algorithmic bytes of
 roofline.recurrent_bytes (state read once and written once per call).
+
+--block times the recurrent block's other operators (short convolution, selective scan, layer
+norm; forward, gradient, and the single-token steps of 256 sequences) on B sequences of T rows
+with D channels and N states, bf16, with roofline's bytes.  Calls rotate over three sets of
+inputs, which together exceed L2.
 """
 from __future__ import annotations
 
@@ -33,8 +39,8 @@ import torch
 
 import kimi_delta_attention_22_b200 as kda
 from kimi_delta_attention_22_b200 import inputs
-from kimi_delta_attention_22_b200.roofline import (backward_bytes, backward_flops, prefill_bytes, prefill_flops,
-                                                   recurrent_bytes)
+from kimi_delta_attention_22_b200.roofline import (backward_bytes, backward_flops, conv_bytes, norm_bytes, prefill_bytes,
+                                                   prefill_flops, recurrent_bytes, ssm_bytes, ssm_exponentials)
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
@@ -214,6 +220,52 @@ def measure_chunk_backward(name: str, iters: int, warmup: int) -> dict:
     return res
 
 
+def measure_block(B: int, T: int, D: int, N: int, iters: int, warmup: int, W: int = 4, steps: int = 256,
+                  H: int = 16) -> list:
+    """One dict per operator of block_ops on B x T rows of D channels (the steps: `steps` sequences)."""
+    rows, sets = B * T, []
+    for seed in range(3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        r = lambda *s: torch.randn(*s, device="cuda", generator=g)  # noqa: E731
+        b = lambda *s: r(*s).to(torch.bfloat16)  # noqa: E731
+        d = dict(x=b(B, T, D), dt=b(B, T, D), z=b(B, T, D), dy=b(B, T, D), B=b(B, T, 1, N), C=b(B, T, 1, N),
+                 A=-torch.arange(1, N + 1, device="cuda", dtype=torch.float32).repeat(D, 1), D=r(D), bias=r(D) - 4.0,
+                 w=0.5 * r(D, W), cb=r(D), nw=1 + 0.1 * r(D), nb=r(D), hw=1 + 0.1 * r(H, D // H), hb=r(H, D // H),
+                 h0=r(B, D, N), cs=b(B, W - 1, D), sx=b(steps, D), sdt=b(steps, D), sz=b(steps, D), sB=b(steps, 1, N),
+                 sC=b(steps, 1, N), sh=r(steps, D, N), scs=b(steps, W - 1, D))
+        _, d["mean"], d["rstd"] = kda.kda_layer_norm_fwd(d["x"], d["nw"], d["nb"])
+        sets.append(d)
+    ssm = lambda d: dict(D=d["D"], z=d["z"], dt_bias=d["bias"], h0=d["h0"])  # noqa: E731
+    calls = {
+        "kda_conv_fwd": (lambda d: kda.kda_conv_fwd(d["x"], d["w"], d["cb"], d["cs"]), conv_bytes(rows, D, W, B)),
+        "kda_conv_bwd": (lambda d: kda.kda_conv_bwd(d["x"], d["w"], d["dy"], d["cb"], d["cs"]),
+                         conv_bytes(rows, D, W, B, backward=True)),
+        "kda_conv_step": (lambda d: kda.kda_conv_step(d["sx"], d["w"], d["scs"], d["cb"]), conv_bytes(steps, D, W, steps)),
+        "kda_ssm_fwd": (lambda d: kda.kda_ssm_fwd(d["x"], d["dt"], d["A"], d["B"], d["C"], **ssm(d)), ssm_bytes(rows, D, N, B)),
+        "kda_ssm_bwd": (lambda d: kda.kda_ssm_bwd(d["x"], d["dt"], d["A"], d["B"], d["C"], d["dy"], **ssm(d)),
+                        ssm_bytes(rows, D, N, B, backward=True)),
+        "kda_ssm_step": (lambda d: kda.kda_ssm_step(d["sx"], d["sdt"], d["A"], d["sB"], d["sC"], d["sh"], D=d["D"], z=d["sz"],
+                                                    dt_bias=d["bias"]), ssm_bytes(steps, D, N, steps)),
+        "kda_layer_norm_fwd": (lambda d: kda.kda_layer_norm_fwd(d["x"], d["nw"], d["nb"]), norm_bytes(rows, D)),
+        "kda_layer_norm_bwd": (lambda d: kda.kda_layer_norm_bwd(d["dy"], d["x"], d["mean"], d["rstd"], d["nw"]),
+                               norm_bytes(rows, D, backward=True)),
+        "kda_layer_norm_fwd per head": (lambda d: kda.kda_layer_norm_fwd(d["x"].unflatten(-1, (H, -1)), d["hw"], d["hb"]),
+                                        norm_bytes(rows, D // H, H)),
+    }
+    pk, out = peaks(), []
+    for name, (call, nbytes) in calls.items():
+        turn = iter(range(1 << 30))
+        ms = _time(lambda: call(sets[next(turn) % 3]), iters, warmup)
+        res = {"kernel": name, "B": B, "T": T, "D": D, "N": N, "ms_per_call": ms, "hbm_gbs": nbytes / (ms * 1e-3) / 1e9,
+               "algorithmic_bytes": nbytes, "iters": iters}
+        if name in ("kda_ssm_fwd", "kda_ssm_bwd"):
+            res["exponentials_per_s"] = ssm_exponentials(rows, D, N, name.endswith("bwd")) / (ms * 1e-3)
+        if pk:
+            res["hbm_frac"] = res["hbm_gbs"] / pk["hbm_gbs"]
+        out.append(res)
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--workloads", default=",".join(n for n in inputs.WORKLOADS))
@@ -227,6 +279,8 @@ def main():
                     help="N,T,H[;N,T,H...]: time kda_recurrent_bwd on these shapes")
     ap.add_argument("--chunk-backward", default=None,
                     help="workload[,workload...]: time kda_chunk_bwd (bf16, d = 128 workloads)")
+    ap.add_argument("--block", action="store_true", help="time the convolution, the selective scan and layer norm")
+    ap.add_argument("--block-shape", default="4,2048,2048,16", help="B,T,D,N of --block (D a multiple of 16)")
     args = ap.parse_args()
     if not torch.cuda.is_available():
         raise SystemExit("measure needs a CUDA device")
@@ -239,6 +293,10 @@ def main():
         for spec in args.backward.split(";"):
             N, T, H = (int(x) for x in spec.split(","))
             print(json.dumps(measure_backward(N, T, H, args.iters, args.warmup)), flush=True)
+        return
+    if args.block:
+        for res in measure_block(*(int(x) for x in args.block_shape.split(",")), args.iters, args.warmup):
+            print(json.dumps(res), flush=True)
         return
     if args.recurrent:
         for T in (int(x) for x in args.tokens.split(",")):

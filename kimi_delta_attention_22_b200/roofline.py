@@ -66,3 +66,41 @@ def backward_flops(w) -> float:
     C, dk, dv = w.chunk, w.d_k, w.d_v
     per_ht = 14 * dk * dv + 5 * C * dv + 5 * C * dk
     return prefill_flops(w) + w.B * w.T * w.H * per_ht
+
+
+# ---- the recurrent block's other operators (rows: token rows of all sequences together; el:
+# bytes per activation; had: whether initial states are passed)
+
+
+def conv_bytes(rows: int, D: int, W: int, seqs: int, el: int = 2, had: bool = True, backward: bool = False) -> int:
+    """kda_conv_fwd (x in, out out, the states, weights and bias once) or kda_conv_bwd (x, d_out in,
+    dx out, states and their gradients, parameters and theirs).  A step is the forward with one
+    row per sequence."""
+    state, params = seqs * (W - 1) * D * el, 4 * D * (W + 1)
+    if backward:
+        return 3 * rows * D * el + 3 * had * state + 2 * params
+    return 2 * rows * D * el + (1 + had) * state + params
+
+
+def ssm_bytes(rows: int, D: int, N: int, seqs: int, G: int = 1, el: int = 2, gate: bool = True, had: bool = True,
+              backward: bool = False) -> int:
+    """kda_ssm_fwd (x, delta, z, B, C in, out out, fp32 states, parameters) or kda_ssm_bwd (d_out as
+    well, and a gradient of each).  A step is the forward with one row per sequence."""
+    state, params = 4 * seqs * D * N, 4 * D * (N + 2)
+    bc = 2 * rows * G * N * el
+    if backward:
+        return (5 + 2 * gate) * rows * D * el + 2 * bc + 3 * had * state + 2 * params
+    return (3 + gate) * rows * D * el + bc + (1 + had) * state + params
+
+
+def ssm_exponentials(rows: int, D: int, N: int, backward: bool = False) -> int:
+    """The decays of kda_ssm_fwd on whole sequences (one per row, channel and state), and of
+    kda_ssm_bwd (two, and one in four rows): what bounds them, at 16 per cycle and SM."""
+    return rows * D * N * 9 // 4 if backward else rows * D * N
+
+
+def norm_bytes(rows: int, D: int, groups: int = 1, el: int = 2, backward: bool = False) -> int:
+    """kda_layer_norm_fwd (x in, out out, weight and bias, mean and rstd) or kda_layer_norm_bwd
+    (d_out, x in, dx out, the weight, its gradient and the bias', mean and rstd)."""
+    e, params, stats = rows * groups * D, 4 * groups * D, 8 * rows * groups
+    return (3 * el * e + 3 * params if backward else 2 * el * e + 2 * params) + stats
