@@ -248,7 +248,7 @@ def kda_conv_fwd(x, weight, bias=None, state=None, cu_seqlens=None, silu: bool =
     out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     fp = None
     if final_state is not None or want_state:
-        final_state, fp = _out(final_state, "final_state", st, x.dtype, dev)
+        final_state, fp = _out(final_state, "final_state", st, x.dtype, dev, x)
     sh = _shape(ConvShape, B, T, D, N, W, _code(x, "x"), 0, int(bool(silu)), xs, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
@@ -297,13 +297,13 @@ def kda_conv_bwd(x, weight, d_out, bias=None, state=None, d_final_state=None, cu
     if d_out.dtype not in (x.dtype, torch.float32):
         raise TypeError(f"d_out must be {x.dtype} or float32, got {d_out.dtype}")
     dp = _want(d_out, "d_out", x.shape, d_out.dtype, dev)
-    dx, dxp = _out(grads.get("dx"), "dx", x.shape, x.dtype, dev)
-    dw, dwp = _out(grads.get("dweight"), "dweight", weight.shape, torch.float32, dev)
+    dx, dxp = _out(grads.get("dx"), "dx", x.shape, x.dtype, dev, x)
+    dw, dwp = _out(grads.get("dweight"), "dweight", weight.shape, torch.float32, dev, weight)
     db = dbp = dst = dstp = None
     if bias is not None:
-        db, dbp = _out(grads.get("dbias"), "dbias", (D,), torch.float32, dev)
+        db, dbp = _out(grads.get("dbias"), "dbias", (D,), torch.float32, dev, weight)
     if want_dstate:
-        dst, dstp = _out(grads.get("dstate"), "dstate", st, x.dtype, dev)
+        dst, dstp = _out(grads.get("dstate"), "dstate", st, x.dtype, dev, x)
     sh = _shape(ConvShape, B, T, D, N, W, _code(x, "x"), _code(d_out, "d_out"), int(bool(silu)), xs, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
@@ -359,7 +359,7 @@ def kda_ssm_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, h0=None, cu_seqlen
     out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     tp = None
     if hT is not None or want_state:
-        hT, tp = _out(hT, "hT", (n, Dc, N), torch.float32, dev)
+        hT, tp = _out(hT, "hT", (n, Dc, N), torch.float32, dev, A)
     sh = _shape(SsmShape, b, T, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
@@ -411,7 +411,7 @@ def kda_ssm_bwd(x, dt, A, B, C, d_out, D=None, z=None, dt_bias=None, h0=None, d_
                                    ("dB", B.shape, like, True), ("dC", B.shape, like, True), ("dD", (Dc,), f32, D is not None),
                                    ("dz", x.shape, like, z is not None), ("ddt_bias", (Dc,), f32, dt_bias is not None),
                                    ("dh0", (n, Dc, N), f32, want_dh0)):
-        r[name], q[name] = _out(grads.get(name), name, shape, dtype, dev) if on else (None, None)
+        r[name], q[name] = _out(grads.get(name), name, shape, dtype, dev, A if dtype is f32 and like is not f32 else x) if on else (None, None)
     sh = _shape(SsmShape, b, T, Dc, N, G, n, _code(x, "x"), int(bool(softplus)), *st, _status_ptr(dev_status, dev))
     lib = lib or _b.load_library()
     with _on(dev):
@@ -457,7 +457,9 @@ def kda_layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, out=None, w
     out, op = _out(out, "out", x.shape, x.dtype, dev, x)
     mean = rstd = mp = rp = None
     if want_stats:
-        mean, rstd = torch.empty((2, *x.shape[:-1]), dtype=torch.float32, device=dev).unbind(0)
+        shape = (2, *x.shape[:-1])
+        f32 = x if x.dtype == torch.float32 else weight
+        mean, rstd = (torch.empty(shape, dtype=torch.float32, device=dev) if f32 is None else f32.new_empty(shape)).unbind(0)
         mp, rp = mean.data_ptr(), rstd.data_ptr()
     sh = _shape(NormShape, rows, G, D, _code(x, "x"), float(eps), xs)
     lib = lib or _b.load_library()
@@ -488,7 +490,7 @@ def kda_layer_norm_bwd(d_out, x, mean, rstd, weight=None, want_params: bool = Tr
     dp = _want(d_out, "d_out", x.shape, x.dtype, dev)
     mp = _want(mean, "mean", x.shape[:-1], torch.float32, dev)
     rp = _want(rstd, "rstd", x.shape[:-1], torch.float32, dev)
-    dx, dxp = _out(grads.get("dx"), "dx", x.shape, x.dtype, dev)
+    dx, dxp = _out(grads.get("dx"), "dx", x.shape, x.dtype, dev, x)
     dw = dwp = db = dbp = None
     if want_params:
         dw, dwp = _out(grads.get("dweight"), "dweight", pshape, torch.float32, dev)
