@@ -94,7 +94,7 @@ cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t s);
 size_t norm_bwd_workspace_bytes(long long rows, int G, int D);
 
-// out_i[c] = sum_k part[k][off_i + c], k in order within each of eight interleaved
+// out_i[c] = sum_k part[k][off_i + c], k in order within each of sixteen interleaved
 // partial sums: the second stage of a parameter gradient's reduction over the rows.
 cudaError_t launch_colsum(const float* part, int K, long long n0, float* out0, long long n1, float* out1,
                           long long n2, float* out2, cudaStream_t s);

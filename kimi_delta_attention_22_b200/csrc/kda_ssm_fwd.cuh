@@ -8,14 +8,20 @@
 // unit gives 16 exponentials per cycle and SM, which bounds the scan; the bytes (x, delta, z,
 // out, once each) take about a third of that time at N = 16.
 //
-// A CTA of 128 threads owns 128 / S channels of one group: S lanes per channel, NS states per
-// lane in registers for all rows.  Rows come in tiles: every thread holds the next tile's x,
-// delta and z of one row and eight channels in registers (loaded while the current tile is
-// scanned), forms dt and dt x in fp32 and lays them down in shared memory [channel][row],
-// where the scan reads four rows at a time; B and C are laid down once per tile for all
-// channels.  The sum over a channel's lanes is taken for four rows at once (the lanes swap
-// halves, so that two exchanges and one more serve four sums).  y goes back through shared
-// memory to the thread that holds the row's x and z.
+// A CTA of 256 threads owns 128 / S channels of one group.  Its first four warps scan: S lanes
+// per channel, NS states per lane in registers for all rows.  The other four stage: rows come
+// in tiles, of which every thread holds the next one's x, delta and z of one row and eight
+// channels in registers while the current tile is scanned; it forms dt and dt x in fp32 and lays
+// them down in shared memory [channel][row], where the scan reads four rows at a time, and B and
+// C as they are, side by side, once per tile for all channels.  Two tile buffers and four named
+// barriers hand the tiles over, so that neither side waits for the other's latencies (243 us with
+// one set of warps doing both, 164 us with two).  The sum over a channel's lanes is taken for
+// four rows at once (the lanes swap halves, so that two exchanges and one more serve four sums).
+// y goes back through shared memory to the thread that holds the row's x and z.
+// 4 x 2048 rows, 2048 channels, 16 states, bf16: 161 us; the exponentials alone (and the gate's
+// and softplus') would take 74 us, the bytes 21 us.  256 CTAs on 148 SMs are 86 % balanced, and
+// on the SMs with two the issue slots are 69 % busy: two scanning warps per scheduler, each a
+// chain along the rows.
 //
 // Too few channels and sequences to fill the SMs: the rows are cut into segments, aligned to
 // the row index and not to sequences.  Pass 1 scans every segment from zero (keeping only the
@@ -329,11 +335,21 @@ __global__ void __launch_bounds__(128) ssm_join_kernel(SsmArgs a, Segments seg, 
     const float A2 = a.A[i] * kLog2e;
     const long long d = i / a.N;
     float h = 0.f;
-#pragma unroll 4
-    for (long long k = 0; k < seg.count; ++k) {
-        const float own = hseg[k * DN + i], dt = dtseg[k * a.D + d];
-        hseg[k * DN + i] = h;
-        h = s_new[k] ? own : fmaf(ex2(dt * A2), h, own);
+    constexpr int U = 8;   // segments whose values are loaded ahead of the chain
+    for (long long k0 = 0; k0 < seg.count; k0 += U) {
+        float own[U], dec[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const bool in = k0 + u < seg.count;
+            own[u] = in ? hseg[(k0 + u) * DN + i] : 0.f;
+            dec[u] = in ? dtseg[(k0 + u) * a.D + d] : 0.f;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (k0 + u >= seg.count) break;
+            hseg[(k0 + u) * DN + i] = h;
+            h = s_new[k0 + u] ? own[u] : fmaf(ex2(dec[u] * A2), h, own[u]);
+        }
     }
 }
 
@@ -353,8 +369,8 @@ int states_for(int N, bool wide) { return wide || N > 32 ? 8 : 4; }
 // those still fill the SMs (two CTAs each), or where the rows are cut, which gives as many CTAs
 // as are wanted.  One segment per sequence of a dense batch (all rows of a packed one) as soon as
 // four states per lane give a CTA per SM: cutting costs a second set of exponentials.
-// 4 x 2048 rows, 2048 channels, 16 states: 162 us whole; 32768 rows, 1024 channels: 489 us cut
-// with four states per lane, see the kernel for the figures with eight.
+// 4 x 2048 rows, 2048 channels, 16 states: 161 us whole with four states per lane, 205 us with
+// eight (128 CTAs).  32768 packed rows, 1024 channels: 436 us cut with eight, 489 us with four.
 Plan plan(long long B, long long T, int D, int N, int G, bool varlen) {
     const long long M = B * T, whole = varlen ? 1 : B;
     auto make = [&](bool wide) {
