@@ -352,6 +352,8 @@ kda_status_t kda_selftest_bounded_wait(int32_t* dev_status, uint32_t budget_us, 
  *   - The inputs named with a stride may be columns of a wider row-major matrix: the
  *     stride is the distance of consecutive rows in elements (0: rows are contiguous).
  *     Everything else is contiguous.
+ *   - Outputs that are passed in place of an input are refused where the kernels would read
+ *     what they have overwritten (KDA_ERR_INVALID_ARG; partial overlaps are the caller's to avoid).
  *   - Every pointer needs its element's alignment.  Where the pointers, strides and
  *     row lengths are multiples of 16 bytes, 16-byte accesses are used.
  *   - Activations and their gradients have the element type `dtype` (fp32 or bf16);
@@ -452,8 +454,8 @@ kda_status_t kda_ssm_fwd(const kda_ssm_shape_t* shape, const void* x, const void
 /* Bytes of workspace (0: none needed); varlen != 0 when a cu_seqlens will be passed. */
 size_t kda_ssm_fwd_workspace_size(const kda_ssm_shape_t* shape, int varlen);
 
-/* kda_ssm_step -- one row for each of B sequences (T == 1): x, delta, z, out [B, D],
- * Bm, Cm [B, G, N]; h [B, D, N] fp32 is read and overwritten with the new state. */
+/* kda_ssm_step -- one row for each of B sequences (T == 1; B up to 131070): x, delta, z,
+ * out [B, D], Bm, Cm [B, G, N]; h [B, D, N] fp32 is read and overwritten with the new state. */
 kda_status_t kda_ssm_step(const kda_ssm_shape_t* shape, const void* x, const void* delta,
                           const float* A, const void* Bm, const void* Cm, const float* Dskip,
                           const void* z, const float* delta_bias, float* h, void* out,
@@ -465,7 +467,9 @@ kda_status_t kda_ssm_step(const kda_ssm_shape_t* shape, const void* x, const voi
  * [rows, D], dB, dC [rows, G, N], dz [rows, D] (with z; else NULL) of dtype, and fp32 dA
  * [D, N], dDskip [D] (with Dskip; else NULL), ddelta_bias [D] (with delta_bias; else
  * NULL), dh0 [num_seqs, D, N] or NULL (not wanted).  The states are computed again from
- * the inputs; nothing is kept from the forward call.
+ * the inputs; nothing is kept from the forward call.  The workspace holds a state for every
+ * four rows and, per block of 64 channels (at N = 16), the rows' partial sums of dB and dC:
+ * about 20 bytes per row and channel at N = 16, in proportion to N.
  */
 kda_status_t kda_ssm_bwd(const kda_ssm_shape_t* shape, const void* x, const void* delta,
                          const float* A, const void* Bm, const void* Cm, const float* Dskip,

@@ -43,10 +43,15 @@ class NormShape(ctypes.Structure):
 
 
 @functools.lru_cache(maxsize=1024)
+def _sizes(cls, *fields):
+    return ctypes.byref(cls(*fields))
+
+
 def _shape(cls, *fields):
     """A shape structure by reference.  The library only reads it, so calls of the same sizes share
-    one: building it takes a good part of the host's time of a small call."""
-    return ctypes.byref(cls(*fields))
+    one (building it takes a good part of the host's time of a small call); one with a status
+    word's address in it is the call's own."""
+    return _sizes(cls, *fields) if fields[-1] is None or cls is NormShape else ctypes.byref(cls(*fields))
 
 
 def declare(lib) -> None:

@@ -119,6 +119,12 @@ __device__ __forceinline__ SeqRange find_seq(const int32_t* cu, int n, long long
         r.ok = true;
         return r;
     }
+    if (n <= 0) {   // a packed batch without sequences: cu has one entry
+        r.q = 0;
+        r.b = r.e = 0;
+        r.ok = false;
+        return r;
+    }
     int lo = 0, hi = n;   // the last i in [0, n) with cu[i] <= t, or 0
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
