@@ -18,10 +18,9 @@
 // one set of warps doing both, 164 us with two).  The sum over a channel's lanes is taken for
 // four rows at once (the lanes swap halves, so that two exchanges and one more serve four sums).
 // y goes back through shared memory to the thread that holds the row's x and z.
-// 4 x 2048 rows, 2048 channels, 16 states, bf16: 161 us; the exponentials alone (and the gate's
+// 4 x 2048 rows, 2048 channels, 16 states, bf16: 140 us; the exponentials alone (and the gate's
 // and softplus') would take 74 us, the bytes 21 us.  256 CTAs on 148 SMs are 86 % balanced, and
-// on the SMs with two the issue slots are 69 % busy: two scanning warps per scheduler, each a
-// chain along the rows.
+// on the SMs with two, the two scanning warps of a scheduler are each a chain along the rows.
 //
 // Too few channels and sequences to fill the SMs: the rows are cut into segments, aligned to
 // the row index and not to sequences.  Pass 1 scans every segment from zero (keeping only the
@@ -271,7 +270,7 @@ __global__ void __launch_bounds__(2 * kThreads, 2) ssm_scan_kernel(SsmArgs a, Se
             Q nq[4][NS / 4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) quads(k, nq[k]);
-#pragma unroll 2
+#pragma unroll   // the whole tile: the scheduler mixes neighbouring rows (161 us for two turns together, 140 for all)
             for (int i = 0; i < TT; i += 4) {
                 const float dts[4] = {nd.x, nd.y, nd.z, nd.w}, us[4] = {nu.x, nu.y, nu.z, nu.w};
                 Q q[4][NS / 4];
@@ -370,7 +369,8 @@ int states_for(int N, bool wide) { return wide || N > 32 ? 8 : 4; }
 // as are wanted.  One segment per sequence of a dense batch (all rows of a packed one) as soon as
 // four states per lane give a CTA per SM: cutting costs a second set of exponentials.
 // 4 x 2048 rows, 2048 channels, 16 states: 161 us whole with four states per lane, 205 us with
-// eight (128 CTAs).  32768 packed rows, 1024 channels: 436 us cut with eight, 489 us with four.
+// eight (128 CTAs); 32768 packed rows, 1024 channels: 442 us cut with eight, 489 us with four
+// (before the tile was unrolled whole: now 140 us and 420 us).
 Plan plan(long long B, long long T, int D, int N, int G, bool varlen) {
     const long long M = B * T, whole = varlen ? 1 : B;
     auto make = [&](bool wide) {
