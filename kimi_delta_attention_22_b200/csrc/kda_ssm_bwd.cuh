@@ -404,10 +404,10 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
 
 // y = 0: hseg[k] (segment k's own last state) -> the state in front of it.
 // y = 1: rseg[k] (what its rows send to the state in front) -> the gradient of its last state.
-// A chain along the segments; sixteen segments' values are loaded ahead of their use.
+// A chain along the segments; eight segments' values are loaded ahead of their use.
 __global__ void __launch_bounds__(128) ssm_bwd_join_kernel(SsmArgs a, int NP, long long K, float* hseg, float* rseg,
                                                            const float* dtseg, const uint8_t* flags) {
-    constexpr int U = 16;
+    constexpr int U = 8;
     const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x, DN = (long long)a.D * NP;
     if (i >= DN) return;
     const long long d = i / NP;
