@@ -26,7 +26,7 @@
 // the row index and not to sequences.  Pass 1 scans every segment from zero (keeping only the
 // last state and the sum of dt), a short pass joins them (the decay over a segment is
 // e^{A sum dt}), pass 2 scans again from the right state.  This doubles the exponentials, so
-// it is used only below one CTA per SM.  32768 packed rows, 1024 channels, 16 states: 422 us
+// it is used only below three CTAs on five SMs.  32768 packed rows, 1024 channels, 16 states: 422 us
 // (summary 183, join 7, final 244 under the profiler; the exponentials twice would take 280).
 #pragma once
 
@@ -385,7 +385,7 @@ Plan plan(long long B, long long T, int D, int N, int G, bool varlen) {
     Plan p = make(true);
     if (blocks(p) * whole >= 2 * kSMs) return p;
     const Plan narrow = make(false);
-    if (blocks(narrow) * whole >= kSMs) return narrow;
+    if (blocks(narrow) * whole >= kSMs * 3 / 5) return narrow;
     long long count = 2LL * kSMs / blocks(p);   // what is resident at once, and no more
     const long long most = M / 128;             // at least 128 rows each
     if (count > most) count = most;
