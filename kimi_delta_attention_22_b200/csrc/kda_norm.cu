@@ -72,14 +72,15 @@ __device__ __forceinline__ long long div_by(long long a, int b) {   // a >= 0; 3
     return a <= 0xffffffffLL ? (long long)((unsigned)a / (unsigned)b) : a / b;
 }
 
-// Whether access c of a lane lies in the row.  The layouts (norm_t) give a row of vector accesses
-// more than half of the lanes' accesses, so only the upper half of them is ever compared; FULL:
-// the row fills all of them.  The comparisons cost more than they look: each keeps the access
-// apart as a branch of its own (65536 x 4096 gradient: 339 us with all, 294 us with none).
+// Whether access c of a lane lies in the row.  The layouts (norm_t) give a row of vector accesses,
+// and every row of more than 32 lanes, more than half of the lanes' accesses, so only the upper
+// half of them is ever compared; FULL: the row fills all of them.  The comparisons cost more
+// than they look: each keeps the access apart as a branch of its own (65536 x 4096 gradient:
+// 339 us with all, 294 us with none).
 template <int VEC, int L, int NC, bool FULL>
 __device__ __forceinline__ bool in_row(int c, int lane, int D) {
     if constexpr (FULL) return true;
-    if (VEC > 1 && c < NC / 2) return true;
+    if ((VEC > 1 || L > 32) && c < NC / 2) return true;
     return (c * L + lane) * VEC < D;
 }
 
@@ -91,7 +92,7 @@ __device__ __forceinline__ void load_params(const float* p, float* o) {
     for (int v = 0; v < VEC; v += PV) unpack<float, PV>(load_pack<PV>(p + v), o + v);
 }
 template <int VEC>
-__device__ __forceinline__ F2 pair(const float* f, int v) { return F2{f[v], VEC > 1 ? f[VEC > 1 ? v + 1 : 0] : 0.f}; }
+__device__ __forceinline__ F2 pair(const float* f, int v) { return F2{f[v], f[v + 1]}; }
 
 template <typename T, int VEC, int L, int NC, bool FULL>
 __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a) {
@@ -196,10 +197,13 @@ constexpr int kStages = 3;   // rows in the ring, one of them being worked on
 // gone over twice in registers as it was loaded, once for its sums and the parameters'
 // gradients, once for dx: unpacking again costs less than the registers of fp32 copies.
 // Threads per SM that the registers are held to where two accesses of a lane leave the choice:
-// three quarters of the warps hide a row's exchanges better than half of them with no spill.
+// three quarters of the warps hide a row's exchanges better than half of them with no spill
+// (of two vector accesses with spills, of eight element accesses without).
 template <int VEC, int L, int NC>
 constexpr int bwd_threads() {
-    return NC * VEC <= 8 ? 1024 : NC == 2 && L > 32 && L <= 256 ? 768 : block_threads<L>() > 512 ? block_threads<L>() : 512;
+    if ((VEC == 1 && NC == 8) || (VEC == 8 && NC == 2 && L > 32 && L <= 256)) return 768;
+    if (NC * VEC <= 8) return 1024;
+    return block_threads<L>() > 512 ? block_threads<L>() : 512;
 }
 
 template <typename T, int VEC, int L, int NC, bool RING, bool FULL>
@@ -313,22 +317,28 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
             unpack<T, VEC>(pg[c], y);
             weights_again(c, wr);
             const float* w = wr;
+            if constexpr (VEC == 1) {
+                const float xh = (x[0] - mu) * rs, gw = y[0] * w[0];
+                dw[c][0] = fmaf(y[0], xh, dw[c][0]);
+                db[c][0] += y[0];
+                s1.x += gw;
+                s2.x = fmaf(gw, xh, s2.x);
+            } else {
 #pragma unroll
-            for (int v = 0; v < VEC; v += (VEC > 1 ? 2 : 1)) {
-                const F2 xh = mul2(add2(pair<VEC>(x, v), both(-mu)), both(rs)), gy = pair<VEC>(y, v);
-                const F2 nw = fma2(gy, xh, pair<VEC>(dw[c], v)), nb = add2(gy, pair<VEC>(db[c], v));
-                dw[c][v] = nw.x;
-                db[c][v] = nb.x;
-                if (VEC > 1) {
-                    dw[c][VEC > 1 ? v + 1 : 0] = nw.y;
-                    db[c][VEC > 1 ? v + 1 : 0] = nb.y;
+                for (int v = 0; v < VEC; v += 2) {
+                    const F2 xh = mul2(add2(pair<VEC>(x, v), both(-mu)), both(rs)), gy = pair<VEC>(y, v);
+                    const F2 nw = fma2(gy, xh, pair<VEC>(dw[c], v)), nb = add2(gy, pair<VEC>(db[c], v));
+                    dw[c][v] = nw.x;
+                    db[c][v] = nb.x;
+                    dw[c][v + 1] = nw.y;
+                    db[c][v + 1] = nb.y;
+                    const F2 gw = mul2(gy, pair<VEC>(w, v));
+                    s1 = add2(s1, gw);
+                    s2 = fma2(gw, xh, s2);
                 }
-                const F2 gw = mul2(gy, pair<VEC>(w, v));
-                s1 = add2(s1, gw);
-                s2 = fma2(gw, xh, s2);
             }
         }
-        const float2 t = row_sum<L>(VEC > 1 ? s1.x + s1.y : s1.x, VEC > 1 ? s2.x + s2.y : s2.x, buf, turn);
+        const float2 t = row_sum<L>(s1.x + s1.y, s2.x + s2.y, buf, turn);
         if (live) {
             // rstd (gw - c1 - xhat c2) = gw rstd + (x k2 + k1), k2 = -c2 rstd^2, k1 = -c1 rstd - mean k2
             const float k2 = -t.y * inv * rs * rs, k1 = fmaf(-mu, k2, -t.x * inv * rs);
@@ -340,12 +350,16 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
                 unpack<T, VEC>(pg[c], y);
                 weights_again(c, wr);
                 const float* w = wr;
+                if constexpr (VEC == 1) {
+                    x[0] = fmaf(y[0] * w[0], rs, fmaf(x[0], k2, k1));
+                } else {
 #pragma unroll
-                for (int v = 0; v < VEC; v += (VEC > 1 ? 2 : 1)) {
-                    const F2 gw = mul2(pair<VEC>(y, v), pair<VEC>(w, v));
-                    const F2 o = fma2(gw, both(rs), fma2(pair<VEC>(x, v), both(k2), both(k1)));
-                    x[v] = o.x;
-                    if (VEC > 1) x[VEC > 1 ? v + 1 : 0] = o.y;
+                    for (int v = 0; v < VEC; v += 2) {
+                        const F2 gw = mul2(pair<VEC>(y, v), pair<VEC>(w, v));
+                        const F2 o = fma2(gw, both(rs), fma2(pair<VEC>(x, v), both(k2), both(k1)));
+                        x[v] = o.x;
+                        x[v + 1] = o.y;
+                    }
                 }
                 store_f32<T, VEC>(on + c * L * VEC, x);
             }
@@ -493,8 +507,19 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
     }
     if (a.D <= 32) KDA_NORM(1, 8, 4);
     if (a.D <= 256) KDA_NORM(1, 32, 8);
-    if (a.D <= 2048) KDA_NORM(1, 256, 8);
-    if (a.D <= 8192) KDA_NORM(1, 1024, 8);
+    // Element accesses: CTAs of few warps with long runs per lane, several of them per SM (one CTA of
+    // 1024 threads has nothing to do while its sums meet).  bf16, 8192 x 4095: forward 147 us with
+    // 1024 lanes, 40 us with 256; gradient 184 and 97 us, of which half by its scalar arithmetic.
+    if (a.D <= 512) KDA_NORM(1, 64, 8);
+    if constexpr (BWD) {
+        if (a.D <= 1024) KDA_NORM(1, 128, 8);
+    } else {
+        if (a.D <= 1024) KDA_NORM(1, 64, 16);
+    }
+    if (a.D <= 2048) KDA_NORM(1, 128, 16);
+    if (a.D <= 4096) KDA_NORM(1, 256, 16);
+    if (a.D <= 8192) KDA_NORM(1, 512, 16);
+    if (a.D <= 16384) KDA_NORM(1, 1024, 16);
     KDA_NORM(1, 1024, 32);
 #undef KDA_NORM
 }
