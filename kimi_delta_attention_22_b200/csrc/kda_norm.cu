@@ -11,7 +11,7 @@
 // registers: the variance is the exact sum over (x - mean)^2, not a difference of moments.
 // The gradient's CTAs walk rows of one group with the parameter gradients of the lane's
 // columns in registers, and write one partial sum each.  bf16: gradient of 65536 x 4096
-// 300 to 320 us, 5.0 to 5.4 TB/s; per-head forward of 131072 x 128 16 us, 4.3 TB/s (of which
+// 305 to 325 us, 4.9 to 5.3 TB/s; per-head forward of 131072 x 128 16 us, 4.3 TB/s (of which
 // launch and tail are 4 us).
 #include "kda_block.cuh"
 
@@ -469,8 +469,8 @@ bool norm_vec(const NormArgs& a, int el) {
            vec_ok(a.d_out, row, 16) && vec_ok(a.dx, row, 16) && vec_ok(a.w, 16, 16) && vec_ok(a.b, 16, 16);
 }
 
-// Lanes per row and accesses per lane: the fewest lanes that hold the row in registers, so
-// that short rows share a warp and no row waits for a barrier that it does not need.
+// Lanes per row and accesses per lane: few lanes that hold the row in registers, so that
+// short rows share a warp and no row waits for a barrier that it does not need.
 template <typename T, bool BWD>
 cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
     constexpr int V = 16 / sizeof(T);
@@ -485,18 +485,29 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
         if (n <= 16) KDA_NORM(V, 8, 2);
         if (n <= 32) KDA_NORM(V, 32, 1);
         if (n <= 64) KDA_NORM(V, 32, 2);
-        if constexpr (BWD) {   // longer runs per lane: the row's sums and copies cost the same for each lane
-            if (n <= 128) KDA_NORM(V, 64, 2);
-            if (n <= 256) KDA_NORM(V, 128, 2);
-            if (n <= 512) KDA_NORM(V, 256, 2);
+        if constexpr (BWD) {
+            // bf16 above 1024 columns: two accesses, as a row's sums and copies cost the same for each
+            // lane (32768 x 4096: one 169 us, two 158, four 244).  fp32, with half the columns per
+            // access, and short rows: one (32768 x 1024 bf16: 68 us with two, 58 with one; fp32 92 and 74)
+            if (n <= 128) KDA_NORM(V, 128, 1);
+            if constexpr (V == 4) {
+                if (n <= 256) KDA_NORM(V, 256, 1);
+                if (n <= 512) KDA_NORM(V, 512, 1);
+            } else {
+                if (n <= 256) KDA_NORM(V, 128, 2);
+                if (n <= 512) KDA_NORM(V, 256, 2);
+            }
             if (n <= 1024) KDA_NORM(V, 512, 2);
             if (n <= 2048) KDA_NORM(V, 512, 4);
         } else {
-            if (n <= 128) KDA_NORM(V, 128, 1);
-            if (n <= 256) KDA_NORM(V, 256, 1);
-            if (n <= 512) KDA_NORM(V, 256, 2);
-            if (n <= 1024) KDA_NORM(V, 512, 2);
-            if (n <= 2048) KDA_NORM(V, 1024, 2);
+            // four accesses per lane: the loads of a row are under way together, and few warps meet in
+            // its sums (bf16, two or one per lane: 32768 x 1024 42 us instead of 29, 32768 x 4096 119
+            // instead of 105, 8192 x 16384 209 instead of 128; eight: 32768 x 2048 64 instead of 55)
+            if (n <= 128) KDA_NORM(V, 32, 4);
+            if (n <= 256) KDA_NORM(V, 64, 4);
+            if (n <= 512) KDA_NORM(V, 128, 4);
+            if (n <= 1024) KDA_NORM(V, 256, 4);
+            if (n <= 2048) KDA_NORM(V, 512, 4);
         }
         if constexpr (V == 4) {
             if (n <= 4096) KDA_NORM(V, 1024, 4);

@@ -38,7 +38,8 @@ SHAPES = [(1, 1, 1, F32), (3, 1, 1, BF), (5, 1, 7, BF), (9, 2, 8, BF), (300, 1, 
           (33, 3, 128, BF), (5, 1, 250, F32), (70, 1, 256, BF), (9, 2, 512, BF), (6, 1, 1000, F32), (5, 1, 1024, BF),
           (4, 1, 1023, BF), (3, 1, 2048, BF), (7, 1, 4096, BF), (3, 1, 4100, F32), (2, 1, 8191, BF), (3, 1, 8192, F32),
           (2, 2, 16384, BF), (2, 1, 16384, F32), (2, 1, 32768, BF), (1, 1, 32768, F32), (1, 1, 32767, F32),
-          (5, 3, 313, BF), (4, 1, 700, F32), (3, 1, 2047, BF), (3, 2, 4095, F32), (3, 1, 4097, BF), (2, 1, 12345, BF)]
+          (5, 3, 313, BF), (4, 1, 700, F32), (3, 1, 2047, BF), (3, 2, 4095, F32), (3, 1, 4097, BF), (2, 1, 12345, BF),
+          (9, 2, 200, F32), (6, 1, 400, F32), (4, 1, 1800, F32), (3, 1, 6000, BF), (3, 1, 2052, F32)]
 
 
 @pytest.mark.gpu
