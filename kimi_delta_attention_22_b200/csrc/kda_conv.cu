@@ -14,74 +14,70 @@
 // 8192 x 6144 74 us, 4.1 TB/s (16 warps per SM, which its 126 registers leave, issue in half of
 // their slots); a step of 256 x 4096 6 us.
 //
-// The tap count is a template parameter WM of {2, 3, 4, 8}; W = 5..7 run on WM = 8 with
-// the leading taps zero.  Taps are aligned at the newest input: tap WM - 1 is row t.
+// The tap count W is a template parameter: the window holds the W - 1 rows in front of the
+// newest and no others (an unused tap of zero would make NaN of an infinity outside the window).
+// Taps are aligned at the newest input: tap W - 1 is row t.
 #include "kda_block.cuh"
 
 namespace kda {
 namespace {
 
-template <int WM, int VEC>
-__device__ __forceinline__ void load_taps(const float* w, const float* bias, int W, long long d0, float (*wr)[VEC],
-                                          float* br) {
-    if (WM == 4 && W == 4 && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {   // one 16-byte load per channel
+template <int W, int VEC>
+__device__ __forceinline__ void load_taps(const float* w, const float* bias, long long d0, float (*wr)[VEC], float* br) {
+    if (W == 4 && (reinterpret_cast<uintptr_t>(w) & 15) == 0) {   // one 16-byte load per channel
 #pragma unroll
         for (int v = 0; v < VEC; ++v) {
             const float4 f = __ldg(reinterpret_cast<const float4*>(w) + d0 + v);
             const float t[4] = {f.x, f.y, f.z, f.w};
 #pragma unroll
-            for (int j = 0; j < WM; ++j) wr[j][v] = t[j & 3];
+            for (int j = 0; j < W; ++j) wr[j][v] = t[j & 3];
         }
     } else {
 #pragma unroll
         for (int v = 0; v < VEC; ++v)
 #pragma unroll
-            for (int j = 0; j < WM; ++j) {
-                const int jj = j - (WM - W);
-                wr[j][v] = jj >= 0 ? __ldg(w + (d0 + v) * W + jj) : 0.f;
-            }
+            for (int j = 0; j < W; ++j) wr[j][v] = __ldg(w + (d0 + v) * W + j);
     }
 #pragma unroll
     for (int v = 0; v < VEC; ++v) br[v] = bias ? __ldg(bias + d0 + v) : 0.f;
 }
 
-// Inputs t - (WM-1) .. t - 1 of the sequence r (from its state in front of row r.b).
-template <typename T, int VEC, int WM>
+// Inputs t - (W-1) .. t - 1 of the sequence r (from its state in front of row r.b).
+template <typename T, int VEC, int W>
 __device__ __forceinline__ void load_window(const ConvArgs& a, const SeqRange& r, long long t, long long d0,
                                             float (*win)[VEC]) {
     const T* x = static_cast<const T*>(a.x) + d0;
     const T* st = static_cast<const T*>(a.state0);
 #pragma unroll
-    for (int j = 0; j < WM - 1; ++j) {
-        const long long p = t - (WM - 1) + j;
+    for (int j = 0; j < W - 1; ++j) {
+        const long long p = t - (W - 1) + j;
         Pack<T, VEC> row = zero_pack<T, VEC>();
         if (p >= r.b) {
             row = load_pack<VEC>(x + p * a.xs);
         } else if (st != nullptr) {
-            const int k = a.W - 1 + (int)(p - r.b);
-            if (k >= 0) row = load_pack<VEC>(st + ((long long)r.q * (a.W - 1) + k) * a.D + d0);
+            row = load_pack<VEC>(st + ((long long)r.q * (W - 1) + (W - 1) + (p - r.b)) * a.D + d0);
         }
         unpack<T, VEC>(row, win[j]);
     }
 }
 
 // The W rows in front of and at row t, in fp32 (unpacked once when a row enters).
-template <int VEC, int WM>
+template <int VEC, int W>
 __device__ __forceinline__ void conv_pre(const float (*win)[VEC], const float* cur, const float (*wr)[VEC], const float* br,
                                          float* pre) {
 #pragma unroll
     for (int v = 0; v < VEC; ++v) pre[v] = br[v];
 #pragma unroll
-    for (int j = 0; j < WM; ++j) fma_n<VEC>(wr[j], j < WM - 1 ? win[j < WM - 1 ? j : 0] : cur, pre);
+    for (int j = 0; j < W; ++j) fma_n<VEC>(wr[j], j < W - 1 ? win[j < W - 1 ? j : 0] : cur, pre);
 }
-template <int VEC, int WM>
+template <int VEC, int W>
 __device__ __forceinline__ void shift_in(float (*win)[VEC], const float* cur) {
 #pragma unroll
-    for (int j = 0; j + 1 < WM - 1; ++j)
+    for (int j = 0; j + 1 < W - 1; ++j)
 #pragma unroll
         for (int v = 0; v < VEC; ++v) win[j][v] = win[j + 1][v];
 #pragma unroll
-    for (int v = 0; v < VEC; ++v) win[WM - 2][v] = cur[v];
+    for (int v = 0; v < VEC; ++v) win[W - 2][v] = cur[v];
 }
 
 constexpr int kU = 4;       // rows worked on together
@@ -89,8 +85,8 @@ constexpr int kAhead = 4;   // groups of kU rows in the ring, one of them being 
 template <typename T, int VEC>
 constexpr int fwd_ring() { return VEC > 1 ? kAhead * kU * 256 * VEC * (int)sizeof(T) : 0; }
 
-template <typename T, int VEC, int WM, bool SILU>
-__global__ void __launch_bounds__(256, WM <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs a, long long run, long long nruns) {
+template <typename T, int VEC, int W, bool SILU>
+__global__ void __launch_bounds__(256, W <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs a, long long run, long long nruns) {
     constexpr bool kFast = sizeof(T) == 2;
     extern __shared__ __align__(16) uint8_t ring_mem[];   // [kAhead][kU][thread]
     T* ring = reinterpret_cast<T*>(ring_mem);
@@ -105,35 +101,35 @@ __global__ void __launch_bounds__(256, WM <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs
         if (q >= a.num_seqs || !check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || a.stateT == nullptr) return;
         const T* st = static_cast<const T*>(a.state0);
         T* fin = static_cast<T*>(a.stateT);
-        for (int j = 0; j < a.W - 1; ++j) {
-            const long long p = e - (a.W - 1) + j;
+        for (int j = 0; j < W - 1; ++j) {
+            const long long p = e - (W - 1) + j;
             Pack<T, VEC> v = zero_pack<T, VEC>();
             if (p >= b) v = load_pack<VEC>(x + p * a.xs);
-            else if (st != nullptr) v = load_pack<VEC>(st + (q * (a.W - 1) + (a.W - 1) + (p - b)) * a.D + d0);
-            store_pack<T, VEC>(fin + (q * (a.W - 1) + j) * a.D + d0, v);
+            else if (st != nullptr) v = load_pack<VEC>(st + (q * (W - 1) + (W - 1) + (p - b)) * a.D + d0);
+            store_pack<T, VEC>(fin + (q * (W - 1) + j) * a.D + d0, v);
         }
         return;
     }
-    float wr[WM][VEC], br[VEC];
-    load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
+    float wr[W][VEC], br[VEC];
+    load_taps<W, VEC>(a.w, a.bias, d0, wr, br);
     T* out = static_cast<T*>(a.out) + d0;
-    float win[WM - 1][VEC];
+    float win[W - 1][VEC];
 
     long long t = who * run;
     const long long t1 = t + run < a.M ? t + run : a.M;
     auto emit = [&](long long row, const Pack<T, VEC>& raw) {
         float cur[VEC], pre[VEC];
         unpack<T, VEC>(raw, cur);
-        conv_pre<VEC, WM>(win, cur, wr, br, pre);
+        conv_pre<VEC, W>(win, cur, wr, br, pre);
         if (SILU) silu_n<VEC, kFast>(pre);
         store_f32<T, VEC>(out + row * a.D, pre);
-        shift_in<VEC, WM>(win, cur);
+        shift_in<VEC, W>(win, cur);
     };
     while (t < t1) {
         const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, t);
         if (!r.ok) { ++t; continue; }
         const long long stop = t1 < r.e ? t1 : r.e;
-        load_window<T, VEC, WM>(a, r, t, d0, win);
+        load_window<T, VEC, W>(a, r, t, d0, win);
         const int quads = (int)((stop - t) / kU);
         const T* px = x + t * a.xs;
         if constexpr (VEC > 1) {   // kAhead - 1 groups of four rows under way
@@ -177,29 +173,28 @@ __global__ void __launch_bounds__(256, WM <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs
 // share one read of the taps (64 bytes per thread, as much as a sequence's state and input).
 constexpr int kSeqs = 4;
 
-template <typename T, int VEC, int WM, bool SILU>
+template <typename T, int VEC, int W, bool SILU>
 __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
     const int nvec = a.D / VEC;
     const long long idx = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     const long long n0 = idx / nvec * kSeqs, d0 = (idx % nvec) * VEC;
     if (n0 >= a.num_seqs) return;
-    const long long ss = (long long)(a.W - 1) * a.D;   // a sequence's state
+    const long long ss = (long long)(W - 1) * a.D;   // a sequence's state
     T* st = static_cast<T*>(a.stateT) + n0 * ss + d0;
     const T* x = static_cast<const T*>(a.x) + n0 * a.xs + d0;
     T* out = static_cast<T*>(a.out) + n0 * a.D + d0;
-    Pack<T, VEC> win[kSeqs][WM];
+    Pack<T, VEC> win[kSeqs][W];
 #pragma unroll
     for (int q = 0; q < kSeqs; ++q) {
         const bool on = n0 + q < a.num_seqs;
 #pragma unroll
-        for (int j = 0; j < WM - 1; ++j) {
-            const int k = j - (WM - a.W);
-            win[q][j] = on && k >= 0 ? load_pack<VEC>(st + q * ss + (long long)k * a.D) : zero_pack<T, VEC>();
+        for (int j = 0; j < W - 1; ++j) {
+            win[q][j] = on ? load_pack<VEC>(st + q * ss + (long long)j * a.D) : zero_pack<T, VEC>();
         }
-        win[q][WM - 1] = on ? load_pack<VEC>(x + q * a.xs) : zero_pack<T, VEC>();
+        win[q][W - 1] = on ? load_pack<VEC>(x + q * a.xs) : zero_pack<T, VEC>();
     }
-    float wr[WM][VEC], br[VEC];
-    load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
+    float wr[W][VEC], br[VEC];
+    load_taps<W, VEC>(a.w, a.bias, d0, wr, br);
 #pragma unroll
     for (int q = 0; q < kSeqs; ++q) {
         if (n0 + q >= a.num_seqs) break;
@@ -207,7 +202,7 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
 #pragma unroll
         for (int v = 0; v < VEC; ++v) pre[v] = br[v];
 #pragma unroll
-        for (int j = 0; j < WM; ++j) {
+        for (int j = 0; j < W; ++j) {
             float f[VEC];
             unpack<T, VEC>(win[q][j], f);
             fma_n<VEC>(wr[j], f, pre);
@@ -215,25 +210,22 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
         if (SILU) silu_n<VEC, sizeof(T) == 2>(pre);
         store_f32<T, VEC>(out + q * a.D, pre);
 #pragma unroll
-        for (int j = 1; j < WM; ++j) {   // the state moves up by one row
-            const int k = j - 1 - (WM - a.W);
-            if (k >= 0) store_pack<T, VEC>(st + q * ss + (long long)k * a.D, win[q][j]);
-        }
+        for (int j = 1; j < W; ++j) store_pack<T, VEC>(st + q * ss + (long long)(j - 1) * a.D, win[q][j]);   // the state moves up by one row
     }
 }
 
 // Backward.  A CTA owns 32 * VEC channels; its eight warps walk runs of rows and keep
 // their share of dw and db in registers, which are added over the warps at the end and
-// written as one partial sum per CTA.  A run needs dpre of up to WM - 1 rows behind it:
+// written as one partial sum per CTA.  A run needs dpre of up to W - 1 rows behind it:
 // those are computed again (they belong to the next run's dw).
 constexpr int kBwdWarps = 8;
 constexpr int kBwdAhead = 3;
 
-template <typename T, typename TG, int VEC, int WM, bool SILU>
+template <typename T, typename TG, int VEC, int W, bool SILU>
 __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, long long run, long long nruns, int K) {
     constexpr bool kFast = sizeof(T) == 2;
     constexpr int NT = 32 * kBwdWarps;
-    extern __shared__ __align__(16) float red[];   // the ring of rows; at the end [kBwdWarps][WM + 1][VEC][32]
+    extern __shared__ __align__(16) float red[];   // the ring of rows; at the end [kBwdWarps][W + 1][VEC][32]
     T* ring_x = reinterpret_cast<T*>(red);
     TG* ring_g = reinterpret_cast<TG*>(ring_x + kBwdAhead * kU * NT * VEC);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -242,10 +234,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
     const T* x = static_cast<const T*>(a.x) + d0;
     const TG* dy = static_cast<const TG*>(a.d_out) + d0;
     T* dx = static_cast<T*>(a.dx) + d0;
-    float dw[WM][VEC] = {}, db[VEC] = {};
+    float dw[W][VEC] = {}, db[VEC] = {};
     if (live) {
-        float wr[WM][VEC], br[VEC];
-        load_taps<WM, VEC>(a.w, a.bias, a.W, d0, wr, br);
+        float wr[W][VEC], br[VEC];
+        load_taps<W, VEC>(a.w, a.bias, d0, wr, br);
         const T* dfin = static_cast<const T*>(a.d_stateT);
         T* dst = static_cast<T*>(a.dstate0);
         for (long long rr = (long long)blockIdx.y * kBwdWarps + warp; rr < nruns; rr += (long long)K * kBwdWarps) {
@@ -255,27 +247,27 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
                 const SeqRange r = find_seq(a.cu, a.num_seqs, a.M, a.T, p0);
                 if (!r.ok) { ++p0; continue; }
                 const long long p1 = rend < r.e ? rend : r.e;
-                float win[WM - 1][VEC];
-                load_window<T, VEC, WM>(a, r, p0, d0, win);
-                float dp[WM][VEC] = {};   // dp[j] = dpre[t - j]
-                // row t enters; row s = t - (WM-1) has all of its gradients and leaves.  `edge`: s may lie
+                float win[W - 1][VEC];
+                load_window<T, VEC, W>(a, r, p0, d0, win);
+                float dp[W][VEC] = {};   // dp[j] = dpre[t - j]
+                // row t enters; row s = t - (W-1) has all of its gradients and leaves.  `edge`: s may lie
                 // in front of the piece (the state's gradient, or another run's row) or be one of the
                 // last W - 1 rows, which the final state holds.
                 auto leave = [&](long long t, bool edge) {
-                    const long long s = t - (WM - 1);
+                    const long long s = t - (W - 1);
                     T* to = dx + s * a.D;
                     float g[VEC] = {};
                     if (edge) {
                         if (s < p0) {
-                            if (p0 != r.b || dst == nullptr || s - r.b < -(a.W - 1)) return;
-                            to = dst + ((long long)r.q * (a.W - 1) + (a.W - 1) + (s - r.b)) * a.D + d0;
+                            if (p0 != r.b || dst == nullptr) return;
+                            to = dst + ((long long)r.q * (W - 1) + (W - 1) + (s - r.b)) * a.D + d0;
                         }
-                        const long long k = s - r.e + (a.W - 1);   // the row is the final state's k-th
+                        const long long k = s - r.e + (W - 1);   // the row is the final state's k-th
                         if (dfin != nullptr && k >= 0)
-                            unpack<T, VEC>(load_pack<VEC>(dfin + ((long long)r.q * (a.W - 1) + k) * a.D + d0), g);
+                            unpack<T, VEC>(load_pack<VEC>(dfin + ((long long)r.q * (W - 1) + k) * a.D + d0), g);
                     }
 #pragma unroll
-                    for (int j = 0; j < WM; ++j) fma_n<VEC>(wr[j], dp[j], g);
+                    for (int j = 0; j < W; ++j) fma_n<VEC>(wr[j], dp[j], g);
                     store_f32<T, VEC>(to, g);
                 };
                 auto enter = [&](const Pack<T, VEC>& cur, const Pack<TG, VEC>& gcur, bool mine) {
@@ -284,7 +276,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
                     unpack<TG, VEC>(gcur, g);
                     if (SILU) {
                         float pre[VEC], sg[VEC];
-                        conv_pre<VEC, WM>(win, cf, wr, br, pre);
+                        conv_pre<VEC, W>(win, cf, wr, br, pre);
                         sigmoid_n<VEC, kFast>(pre, sg);
                         if constexpr (VEC > 1) {
 #pragma unroll
@@ -299,7 +291,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
                         }
                     }
 #pragma unroll
-                    for (int j = WM - 1; j > 0; --j)
+                    for (int j = W - 1; j > 0; --j)
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) dp[j][v] = dp[j - 1][v];
 #pragma unroll
@@ -308,9 +300,9 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
 #pragma unroll
                         for (int v = 0; v < VEC; ++v) db[v] += g[v];
 #pragma unroll
-                        for (int j = 0; j < WM; ++j) fma_n<VEC>(g, j < WM - 1 ? win[j < WM - 1 ? j : 0] : cf, dw[j]);
+                        for (int j = 0; j < W; ++j) fma_n<VEC>(g, j < W - 1 ? win[j < W - 1 ? j : 0] : cf, dw[j]);
                     }
-                    shift_in<VEC, WM>(win, cf);
+                    shift_in<VEC, W>(win, cf);
                 };
                 long long t = p0;
                 const int quads = (int)((p1 - p0) / kU);
@@ -347,7 +339,7 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
                     }
                     ahead(q + kBwdAhead - 1, slot == 0 ? kBwdAhead - 1 : slot - 1);
                     slot = slot == kBwdAhead - 1 ? 0 : slot + 1;
-                    if (q * kU >= WM - 1) {   // inside: s is a row of the piece, W or more in front of the end
+                    if (q * kU >= W - 1) {   // inside: s is a row of the piece, W or more in front of the end
 #pragma unroll
                         for (int u = 0; u < kU; ++u) {
                             enter(cx[u], cg[u], true);
@@ -366,12 +358,12 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
                     enter(load_pack<VEC>(x + t * a.xs), load_pack<VEC>(dy + t * a.D), true);
                     leave(t, true);
                 }
-                for (; t < p1 + WM - 1; ++t) {   // behind the piece: another run's rows, or past the sequence's end
+                for (; t < p1 + W - 1; ++t) {   // behind the piece: another run's rows, or past the sequence's end
                     if (t < r.e) {
                         enter(load_pack<VEC>(x + t * a.xs), load_pack<VEC>(dy + t * a.D), false);
                     } else {
 #pragma unroll
-                        for (int j = WM - 1; j > 0; --j)
+                        for (int j = W - 1; j > 0; --j)
 #pragma unroll
                             for (int v = 0; v < VEC; ++v) dp[j][v] = dp[j - 1][v];
 #pragma unroll
@@ -386,10 +378,10 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
         for (long long q = (long long)blockIdx.y * kBwdWarps + warp; q < a.num_seqs; q += (long long)K * kBwdWarps) {
             long long b, e;
             if (!check_seq(a.cu, (int)q, a.M, a.T, a.dev_status, b, e) || b != e || dst == nullptr) continue;
-            for (int j = 0; j < a.W - 1; ++j) {
+            for (int j = 0; j < W - 1; ++j) {
                 Pack<T, VEC> v = zero_pack<T, VEC>();
-                if (dfin != nullptr) v = load_pack<VEC>(dfin + (q * (a.W - 1) + j) * a.D + d0);
-                store_pack<T, VEC>(dst + (q * (a.W - 1) + j) * a.D + d0, v);
+                if (dfin != nullptr) v = load_pack<VEC>(dfin + (q * (W - 1) + j) * a.D + d0);
+                store_pack<T, VEC>(dst + (q * (W - 1) + j) * a.D + d0, v);
             }
         }
     }
@@ -397,21 +389,21 @@ __global__ void __launch_bounds__(32 * kBwdWarps) conv_bwd_kernel(ConvArgs a, lo
 #pragma unroll
     for (int v = 0; v < VEC; ++v) {
 #pragma unroll
-        for (int j = 0; j < WM; ++j) red[((warp * (WM + 1) + j) * VEC + v) * 32 + lane] = dw[j][v];
-        red[((warp * (WM + 1) + WM) * VEC + v) * 32 + lane] = db[v];
+        for (int j = 0; j < W; ++j) red[((warp * (W + 1) + j) * VEC + v) * 32 + lane] = dw[j][v];
+        red[((warp * (W + 1) + W) * VEC + v) * 32 + lane] = db[v];
     }
     __syncthreads();
     // part[blockIdx.y]: [D][W] of dw, then [D] of db
-    float* part = a.part + (long long)blockIdx.y * a.D * (a.W + 1);
-    for (int i = threadIdx.x; i < (WM + 1) * VEC * 32; i += blockDim.x) {
+    float* part = a.part + (long long)blockIdx.y * a.D * (W + 1);
+    for (int i = threadIdx.x; i < (W + 1) * VEC * 32; i += blockDim.x) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < kBwdWarps; ++w) s += red[w * (WM + 1) * VEC * 32 + i];
+        for (int w = 0; w < kBwdWarps; ++w) s += red[w * (W + 1) * VEC * 32 + i];
         const int j = i / (VEC * 32), v = (i / 32) % VEC, l = i & 31;
         const long long d = ((long long)blockIdx.x * 32 + l) * VEC + v;
         if (d >= a.D) continue;
-        if (j == WM) part[(long long)a.D * a.W + d] = s;
-        else if (j >= WM - a.W) part[d * a.W + (j - (WM - a.W))] = s;
+        if (j == W) part[(long long)a.D * W + d] = s;
+        else part[d * W + j] = s;
     }
 }
 
@@ -428,7 +420,7 @@ struct BwdPlan {
     long long run, nruns;
 };
 // One run of consecutive rows per warp, as many CTAs as are resident at once (two per SM): the
-// rows divide evenly and the WM - 1 rows behind a run, computed twice, are few.
+// rows divide evenly and the W - 1 rows behind a run, computed twice, are few.
 BwdPlan bwd_plan(long long M, int D, int vec) {
     BwdPlan p;
     const long long nblk = (D + 32LL * vec - 1) / (32LL * vec);
@@ -453,6 +445,9 @@ cudaError_t fwd_w(const ConvArgs& a, cudaStream_t s) {
     auto k = a.W == 2   ? conv_fwd_kernel<T, VEC, 2, SILU>
              : a.W == 3 ? conv_fwd_kernel<T, VEC, 3, SILU>
              : a.W == 4 ? conv_fwd_kernel<T, VEC, 4, SILU>
+             : a.W == 5 ? conv_fwd_kernel<T, VEC, 5, SILU>
+             : a.W == 6 ? conv_fwd_kernel<T, VEC, 6, SILU>
+             : a.W == 7 ? conv_fwd_kernel<T, VEC, 7, SILU>
                         : conv_fwd_kernel<T, VEC, 8, SILU>;
     cudaError_t e;
     if ((e = allow_smem(k, smem)) != cudaSuccess) return e;
@@ -467,18 +462,21 @@ cudaError_t step_w(const ConvArgs& a, cudaStream_t s) {
         case 2: conv_step_kernel<T, VEC, 2, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
         case 3: conv_step_kernel<T, VEC, 3, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
         case 4: conv_step_kernel<T, VEC, 4, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
+        case 5: conv_step_kernel<T, VEC, 5, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
+        case 6: conv_step_kernel<T, VEC, 6, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
+        case 7: conv_step_kernel<T, VEC, 7, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
         default: conv_step_kernel<T, VEC, 8, SILU><<<(unsigned)grid, 256, 0, s>>>(a); break;
     }
     return cudaGetLastError();
 }
-template <typename T, typename TG, int VEC, int WM, bool SILU>
+template <typename T, typename TG, int VEC, int W, bool SILU>
 cudaError_t bwd_one(const ConvArgs& a, cudaStream_t s) {
     const BwdPlan p = bwd_plan(a.M, a.D, VEC);
     const dim3 grid((unsigned)((a.D + 32 * VEC - 1) / (32 * VEC)), (unsigned)p.K);
-    constexpr int sums = (int)sizeof(float) * kBwdWarps * (WM + 1) * VEC * 32;
+    constexpr int sums = (int)sizeof(float) * kBwdWarps * (W + 1) * VEC * 32;
     constexpr int ring = VEC > 1 ? kBwdAhead * kU * 32 * kBwdWarps * VEC * (int)(sizeof(T) + sizeof(TG)) : 0;
     constexpr int smem = sums > ring ? sums : ring;
-    auto k = conv_bwd_kernel<T, TG, VEC, WM, SILU>;
+    auto k = conv_bwd_kernel<T, TG, VEC, W, SILU>;
     cudaError_t e = allow_smem(k, smem);
     if (e != cudaSuccess) return e;
     k<<<grid, 32 * kBwdWarps, smem, s>>>(a, p.run, p.nruns, p.K);
@@ -492,6 +490,9 @@ cudaError_t bwd_w(const ConvArgs& a, cudaStream_t s) {
         case 2: return bwd_one<T, TG, VEC, 2, SILU>(a, s);
         case 3: return bwd_one<T, TG, VEC, 3, SILU>(a, s);
         case 4: return bwd_one<T, TG, VEC, 4, SILU>(a, s);
+        case 5: return bwd_one<T, TG, VEC, 5, SILU>(a, s);
+        case 6: return bwd_one<T, TG, VEC, 6, SILU>(a, s);
+        case 7: return bwd_one<T, TG, VEC, 7, SILU>(a, s);
         default: return bwd_one<T, TG, VEC, 8, SILU>(a, s);
     }
 }
