@@ -177,6 +177,8 @@ kda_status_t kda_conv_bwd(const kda_conv_shape_t* sh, const void* x, const float
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
     if (a.M > 0 && (dx == x || dx == d_out)) return KDA_ERR_INVALID_ARG;
+    // a sequence's other runs read its state and its final state's gradient while dstate0 is stored
+    if (dstate0 != nullptr && (dstate0 == state0 || dstate0 == d_stateT)) return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.part = reinterpret_cast<float*>(ws);
         return kda::launch_conv_bwd(a, sh->dtype == KDA_BF16, sh->grad_dtype == KDA_BF16, sh->activation == 1,
@@ -261,6 +263,8 @@ kda_status_t kda_ssm_bwd(const kda_ssm_shape_t* sh, const void* x, const void* d
     for (const void* g : grads)
         for (const void* i : in)
             if (a.M > 0 && g != nullptr && g == i) return KDA_ERR_INVALID_ARG;
+    // a sequence's last segment reads d_hT while its first one stores dh0 (h0 is read by the storing thread)
+    if (dh0 != nullptr && dh0 == d_hT) return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.ws = ws;
         return kda::launch_ssm_bwd(a, sh->dtype == KDA_BF16, static_cast<cudaStream_t>(stream));
