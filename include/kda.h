@@ -352,8 +352,11 @@ kda_status_t kda_selftest_bounded_wait(int32_t* dev_status, uint32_t budget_us, 
  *   - The inputs named with a stride may be columns of a wider row-major matrix: the
  *     stride is the distance of consecutive rows in elements (0: rows are contiguous).
  *     Everything else is contiguous.
- *   - Outputs that are passed in place of an input are refused where the kernels would read
- *     what they have overwritten (KDA_ERR_INVALID_ARG; partial overlaps are the caller's to avoid).
+ *   - An output that starts in an input's place is refused (KDA_ERR_INVALID_ARG) where threads
+ *     may read what others have overwritten.  In place are taken: out of a step on x, delta or z
+ *     and out or dx of layer norm on x, each with rows at the same distance, dx of layer norm
+ *     on d_out, dh0 on h0, and a parameter's gradient on the parameter.
+ *     Overlaps that do not start at the same address are the caller's to avoid.
  *   - Every pointer needs its element's alignment.  Where the pointers, strides and
  *     row lengths are multiples of 16 bytes, 16-byte accesses are used.
  *   - Activations and their gradients have the element type `dtype` (fp32 or bf16);

@@ -1,6 +1,7 @@
 // kda_block_api.cu -- the C entry points of the recurrent block's operators: host-side
 // validation and scratch.  As in kda_api.cu, every check runs before any launch and nothing
 // synchronises; scratch without a caller workspace comes from the stream-ordered pool.
+#include <initializer_list>
 #include <stdint.h>
 
 #include "kda_block.cuh"
@@ -23,6 +24,19 @@ unsigned el_of(int t) { return t == KDA_BF16 ? 2u : 4u; }
 bool batch_ok(int B, int T, int num_seqs, bool varlen) {
     if (B < 0 || T < 0 || num_seqs < 0) return false;
     return varlen ? B == 1 : num_seqs == B;
+}
+
+// Whether an output starts in an input's place.
+bool in_place(std::initializer_list<const void*> outs, std::initializer_list<const void*> ins) {
+    for (const void* o : outs)
+        for (const void* i : ins)
+            if (o != nullptr && o == i) return true;
+    return false;
+}
+// The same for an output whose elements are stored by the thread that read the input's elements at
+// the same index: in place is then right where consecutive rows of both lie `row` elements apart.
+bool rows_shifted(const void* out, const void* in, long long rows, long long stride, long long row) {
+    return out != nullptr && out == in && rows > 1 && stride != row;
 }
 
 kda_status_t check_workspace(const void* ws, size_t have, size_t need) {
@@ -127,12 +141,11 @@ kda_status_t kda_conv_fwd(const kda_conv_shape_t* sh, const void* x, const float
     kda::ConvArgs a = conv_args(sh, x, weight, bias, state0, cu_seqlens);
     a.out = out; a.stateT = stateT;
     if (!weight || (a.M > 0 && (!x || !out))) return KDA_ERR_INVALID_ARG;
-    if (stateT != nullptr && stateT == state0) return KDA_ERR_INVALID_ARG;
     const unsigned el = el_of(sh->dtype);
     if (!aligned(x, el) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(state0, el) || !aligned(cu_seqlens, 4) ||
         !aligned(out, el) || !aligned(stateT, el))
         return KDA_ERR_MISALIGNED;
-    if (a.M > 0 && out == x) return KDA_ERR_INVALID_ARG;
+    if (in_place({stateT}, {state0}) || (a.M > 0 && in_place({out, stateT}, {x, state0, weight, bias}))) return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return status_of(kda::launch_conv_fwd(a, sh->dtype == KDA_BF16, sh->activation == 1, static_cast<cudaStream_t>(stream)));
 }
@@ -148,6 +161,9 @@ kda_status_t kda_conv_step(const kda_conv_shape_t* sh, const void* x, const floa
     const unsigned el = el_of(sh->dtype);
     if (!aligned(x, el) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(out, el) || !aligned(state, el))
         return KDA_ERR_MISALIGNED;
+    if (a.M > 0 && (in_place({out}, {state, weight, bias}) || in_place({state}, {x, weight, bias}) ||
+                    rows_shifted(out, x, a.M, a.xs, a.D)))
+        return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return status_of(kda::launch_conv_step(a, sh->dtype == KDA_BF16, sh->activation == 1, static_cast<cudaStream_t>(stream)));
 }
@@ -176,9 +192,11 @@ kda_status_t kda_conv_bwd(const kda_conv_shape_t* sh, const void* x, const float
     const size_t need = kda_conv_bwd_workspace_size(sh);
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
-    if (a.M > 0 && (dx == x || dx == d_out)) return KDA_ERR_INVALID_ARG;
-    // a sequence's other runs read its state and its final state's gradient while dstate0 is stored
-    if (dstate0 != nullptr && (dstate0 == state0 || dstate0 == d_stateT)) return KDA_ERR_INVALID_ARG;
+    // runs read rows, states and their gradients that others store gradients over (those of the
+    // parameters are stored behind the last read of anything)
+    if (in_place({dstate0}, {state0, d_stateT}) ||
+        (a.M > 0 && in_place({dx, dstate0}, {x, d_out, state0, d_stateT, weight, bias})))
+        return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.part = reinterpret_cast<float*>(ws);
         return kda::launch_conv_bwd(a, sh->dtype == KDA_BF16, sh->grad_dtype == KDA_BF16, sh->activation == 1,
@@ -200,13 +218,12 @@ kda_status_t kda_ssm_fwd(const kda_ssm_shape_t* sh, const void* x, const void* d
     kda::SsmArgs a = ssm_args(sh, x, delta, A, Bm, Cm, Dskip, z, delta_bias, h0, cu_seqlens);
     a.out = out; a.hT = hT;
     if (!A || (a.M > 0 && (!x || !delta || !Bm || !Cm || !out))) return KDA_ERR_INVALID_ARG;
-    if (hT != nullptr && hT == h0) return KDA_ERR_INVALID_ARG;
     const unsigned el = el_of(sh->dtype);
     if (!ssm_pointers_aligned(a, el) || !aligned(out, el) || !aligned(hT, 4)) return KDA_ERR_MISALIGNED;
     const size_t need = kda_ssm_fwd_workspace_size(sh, cu_seqlens != nullptr);
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
-    if (a.M > 0 && (out == x || out == delta || out == z)) return KDA_ERR_INVALID_ARG;
+    if (in_place({hT}, {h0}) || (a.M > 0 && in_place({out, hT}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, h0}))) return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.ws = ws;
@@ -225,6 +242,10 @@ kda_status_t kda_ssm_step(const kda_ssm_shape_t* sh, const void* x, const void* 
     if (!A || (a.M > 0 && (!x || !delta || !Bm || !Cm || !out || !h))) return KDA_ERR_INVALID_ARG;
     const unsigned el = el_of(sh->dtype);
     if (!ssm_pointers_aligned(a, el) || !aligned(out, el) || !aligned(h, 4)) return KDA_ERR_MISALIGNED;
+    if (a.M > 0 && (in_place({out}, {Bm, Cm, A, Dskip, delta_bias, h}) || in_place({h}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias}) ||
+                    rows_shifted(out, x, a.M, a.xs, a.D) || rows_shifted(out, delta, a.M, a.ds, a.D) ||
+                    rows_shifted(out, z, a.M, a.zs, a.D)))
+        return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return status_of(kda::launch_ssm_step(a, sh->dtype == KDA_BF16, static_cast<cudaStream_t>(stream)));
 }
@@ -258,13 +279,12 @@ kda_status_t kda_ssm_bwd(const kda_ssm_shape_t* sh, const void* x, const void* d
     const size_t need = kda_ssm_bwd_workspace_size(sh, cu_seqlens != nullptr);
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
-    const void* const in[] = {x, delta, z, Bm, Cm, d_out};
-    const void* const grads[] = {dx, ddelta, dz, dB, dC};
-    for (const void* g : grads)
-        for (const void* i : in)
-            if (a.M > 0 && g != nullptr && g == i) return KDA_ERR_INVALID_ARG;
-    // a sequence's last segment reads d_hT while its first one stores dh0 (h0 is read by the storing thread)
-    if (dh0 != nullptr && dh0 == d_hT) return KDA_ERR_INVALID_ARG;
+    // segments read what others store gradients over; only h0 is read by the thread that stores dh0
+    // (and the parameters' gradients are stored behind the last read of anything)
+    if (in_place({dh0}, {d_hT}) ||
+        (a.M > 0 && (in_place({dx, ddelta, dz, dB, dC}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, h0, d_out, d_hT}) ||
+                     in_place({dh0}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, d_out}))))
+        return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.ws = ws;
         return kda::launch_ssm_bwd(a, sh->dtype == KDA_BF16, static_cast<cudaStream_t>(stream));
@@ -282,10 +302,13 @@ kda_status_t kda_layer_norm_fwd(const kda_norm_shape_t* sh, const void* x, const
         !aligned(rstd, 4))
         return KDA_ERR_MISALIGNED;
     if (sh->rows == 0) return KDA_OK;
+    if (in_place({out, mean, rstd}, {weight, bias}) || in_place({mean, rstd}, {x})) return KDA_ERR_INVALID_ARG;
     kda::NormArgs a{};
     a.x = x; a.w = weight; a.b = bias; a.out = out; a.mean = mean; a.rstd = rstd;
     a.rows = sh->rows; a.G = sh->groups; a.D = sh->D; a.eps = sh->eps;
-    a.xs = sh->x_stride != 0 ? sh->x_stride : (long long)sh->groups * sh->D;
+    const long long row = (long long)sh->groups * sh->D;
+    a.xs = sh->x_stride != 0 ? sh->x_stride : row;
+    if (rows_shifted(out, x, a.rows, a.xs, row)) return KDA_ERR_INVALID_ARG;
     return status_of(kda::launch_norm_fwd(a, sh->dtype == KDA_BF16, static_cast<cudaStream_t>(stream)));
 }
 
@@ -313,7 +336,9 @@ kda_status_t kda_layer_norm_bwd(const kda_norm_shape_t* sh, const void* d_out, c
     a.d_out = d_out; a.x = x; a.w = weight; a.mean = const_cast<float*>(mean); a.rstd = const_cast<float*>(rstd);
     a.dx = dx; a.dw = dweight; a.db = dbias;
     a.rows = sh->rows; a.G = sh->groups; a.D = sh->D;
-    a.xs = sh->x_stride != 0 ? sh->x_stride : (long long)sh->groups * sh->D;
+    const long long row = (long long)sh->groups * sh->D;
+    a.xs = sh->x_stride != 0 ? sh->x_stride : row;
+    if (a.rows > 0 && (in_place({dx}, {weight, mean, rstd}) || rows_shifted(dx, x, a.rows, a.xs, row))) return KDA_ERR_INVALID_ARG;
     return with_workspace(need ? workspace : nullptr, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.part = reinterpret_cast<float*>(ws);
         return kda::launch_norm_bwd(a, sh->dtype == KDA_BF16, static_cast<cudaStream_t>(stream));
