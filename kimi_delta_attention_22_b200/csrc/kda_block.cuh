@@ -160,21 +160,29 @@ struct Pack {
     static constexpr int kWords = VEC * (int)sizeof(T) / 4 > 0 ? VEC * (int)sizeof(T) / 4 : 1;
     uint32_t w[kWords];
 };
-template <int VEC, typename T>
+// READ_ONLY: the read-only path, for what no thread stores while the kernel runs.  A tensor that the
+// kernel may store in place is read by plain loads, which stay in front of this thread's stores.
+template <bool READ_ONLY, typename W>
+__device__ __forceinline__ W load_word(const void* p) {
+    const W* w = static_cast<const W*>(p);
+    if constexpr (READ_ONLY) return __ldg(w);
+    else return *w;
+}
+template <int VEC, bool READ_ONLY = true, typename T>
 __device__ __forceinline__ Pack<T, VEC> load_pack(const T* p) {
     Pack<T, VEC> r;
     if constexpr (VEC * sizeof(T) == 16) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+        const uint4 v = load_word<READ_ONLY, uint4>(p);
         r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
     } else if constexpr (VEC * sizeof(T) == 8) {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+        const uint2 v = load_word<READ_ONLY, uint2>(p);
         r.w[0] = v.x; r.w[1] = v.y;
     } else if constexpr (sizeof(T) == 2) {
         static_assert(VEC == 1, "one element");
-        r.w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+        r.w[0] = load_word<READ_ONLY, unsigned short>(p);
     } else {
         static_assert(VEC == 1, "one element");
-        r.w[0] = __ldg(reinterpret_cast<const unsigned int*>(p));
+        r.w[0] = load_word<READ_ONLY, unsigned int>(p);
     }
     return r;
 }

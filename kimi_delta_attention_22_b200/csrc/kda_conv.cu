@@ -170,7 +170,8 @@ __global__ void __launch_bounds__(256, W <= 4 ? 3 : 1) conv_fwd_kernel(ConvArgs 
 }
 
 // One row: a thread takes its channels of kSeqs sequences, whose loads are under way together and
-// share one read of the taps (64 bytes per thread, as much as a sequence's state and input).
+// share one read of the taps (64 bytes per thread, as much as a sequence's state and input).  The
+// state is stored in place, and out may be x: plain loads of both.
 constexpr int kSeqs = 4;
 
 template <typename T, int VEC, int W, bool SILU>
@@ -189,9 +190,9 @@ __global__ void __launch_bounds__(256) conv_step_kernel(ConvArgs a) {
         const bool on = n0 + q < a.num_seqs;
 #pragma unroll
         for (int j = 0; j < W - 1; ++j) {
-            win[q][j] = on ? load_pack<VEC>(st + q * ss + (long long)j * a.D) : zero_pack<T, VEC>();
+            win[q][j] = on ? load_pack<VEC, false>(st + q * ss + (long long)j * a.D) : zero_pack<T, VEC>();
         }
-        win[q][W - 1] = on ? load_pack<VEC>(x + q * a.xs) : zero_pack<T, VEC>();
+        win[q][W - 1] = on ? load_pack<VEC, false>(x + q * a.xs) : zero_pack<T, VEC>();
     }
     float wr[W][VEC], br[VEC];
     load_taps<W, VEC>(a.w, a.bias, d0, wr, br);

@@ -9,6 +9,7 @@
 // (row, group), each lane NC accesses of VEC elements (one access: 16 bytes, or one
 // element where rows do not start on 16 bytes), so that the row is read once and stays in
 // registers: the variance is the exact sum over (x - mean)^2, not a difference of moments.
+// out may be x, and dx x or d_out: these are read by plain loads (or copies ahead, of other rows).
 // The gradient's CTAs walk rows of one group with the parameter gradients of the lane's
 // columns in registers, and write one partial sum each.  bf16: gradient of 65536 x 4096
 // 305 to 325 us, 4.9 to 5.3 TB/s; per-head forward of 131072 x 128 16 us, 4.3 TB/s (of which
@@ -112,7 +113,7 @@ __global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
             const int d = (c * L + lane) * VEC;
-            px[r][c] = live && in_row<VEC, L, NC, FULL>(c, lane, a.D) ? load_pack<VEC>(xg + (row0 + r) * a.xs + d) : zero_pack<T, VEC>();
+            px[r][c] = live && in_row<VEC, L, NC, FULL>(c, lane, a.D) ? load_pack<VEC, false>(xg + (row0 + r) * a.xs + d) : zero_pack<T, VEC>();
         }
     }
     float w[NC][VEC], b[NC][VEC];
@@ -290,8 +291,8 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
                 px[c] = lds_pack<T, VEC>(&ring[((st * 2 + 0) * NC + c) * NT + threadIdx.x]);
                 pg[c] = lds_pack<T, VEC>(&ring[((st * 2 + 1) * NC + c) * NT + threadIdx.x]);
             } else {
-                px[c] = load_pack<VEC>(xn + c * L * VEC);
-                pg[c] = load_pack<VEC>(yn + c * L * VEC);
+                px[c] = load_pack<VEC, false>(xn + c * L * VEC);
+                pg[c] = load_pack<VEC, false>(yn + c * L * VEC);
             }
         }
         if constexpr (RING) {
