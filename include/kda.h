@@ -348,7 +348,11 @@ kda_status_t kda_selftest_bounded_wait(int32_t* dev_status, uint32_t budget_us, 
  *     batch (cu_seqlens as in kda_chunk_fwd: device int32 [num_seqs + 1], B == 1).
  *     Sequence n starts from its own state and never sees another sequence's rows.
  *     Rows that no sequence covers are left untouched.  An inconsistent cu_seqlens sets
- *     KDA_DEV_BAD_SEQLENS; the sequences it affects are skipped.
+ *     KDA_DEV_BAD_SEQLENS, and nothing outside the call's tensors is touched.  Sequence n is
+ *     skipped where 0 <= cu[n-1] <= cu[n] <= cu[n+1] <= T fails (or cu[0] is not 0): its states
+ *     and the rows that only skipped sequences claim are left untouched.  A sequence with no
+ *     larger bound in front of it and no smaller one behind it keeps its results; those of the
+ *     remaining sequences, and the parameters' gradients, are then unspecified.
  *   - The inputs named with a stride may be columns of a wider row-major matrix: the
  *     stride is the distance of consecutive rows in elements (0: rows are contiguous).
  *     Everything else is contiguous.

@@ -108,8 +108,9 @@ struct SeqRange {
 };
 
 // The sequence of row t (0 <= t < M).  Dense: t / T.  Packed: the last n with
-// cu[n] <= t, which skips empty sequences; bounds that break the rules give ok = false,
-// so that no address is ever formed from them.
+// cu[n] <= t, which skips empty sequences; bounds that break the rules, the begin in front among
+// them (a sequence that starts inside an earlier one), give ok = false, so that no address is
+// ever formed from them.
 __device__ __forceinline__ SeqRange find_seq(const int32_t* cu, int n, long long M, long long T, long long t) {
     SeqRange r;
     if (cu == nullptr) {
@@ -131,9 +132,10 @@ __device__ __forceinline__ SeqRange find_seq(const int32_t* cu, int n, long long
         if (__ldg(cu + mid) <= t) lo = mid; else hi = mid;
     }
     r.q = lo;
-    r.b = __ldg(cu + lo);
-    r.e = __ldg(cu + lo + 1);
-    r.ok = r.b >= 0 && r.b <= t && t < r.e && r.e <= M && !(lo == 0 && r.b != 0);
+    const int p = __ldg(cu + (lo > 0 ? lo - 1 : 0)), b = __ldg(cu + lo), e = __ldg(cu + lo + 1);
+    r.b = b;
+    r.e = e;
+    r.ok = b >= 0 && p <= b && b <= t && t < e && e <= M && (lo > 0 || b == 0);
     return r;
 }
 
@@ -147,7 +149,8 @@ __device__ __forceinline__ bool check_seq(const int32_t* cu, int q, long long M,
     }
     b = __ldg(cu + q);
     e = __ldg(cu + q + 1);
-    if (b < 0 || e < b || e > M || (q == 0 && b != 0)) {
+    const long long before = q > 0 ? __ldg(cu + q - 1) : b;
+    if (b < 0 || b < before || e < b || e > M || (q == 0 && b != 0)) {
         if (dev_status) atomicOr(dev_status, KDA_DEV_BAD_SEQLENS);
         return false;
     }
