@@ -341,8 +341,10 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
         }
         const float2 t = row_sum<L>(s1.x + s1.y, s2.x + s2.y, buf, turn);
         if (live) {
-            // rstd (gw - c1 - xhat c2) = gw rstd + (x k2 + k1), k2 = -c2 rstd^2, k1 = -c1 rstd - mean k2
-            const float k2 = -t.y * inv * rs * rs, k1 = fmaf(-mu, k2, -t.x * inv * rs);
+            // rstd (gw - c1 - xhat c2) = gw rstd + ((x - mean) k2 + k1), k2 = -c2 rstd^2, k1 = -c1 rstd.  The
+            // mean is taken from x first: x k2 + (k1 - mean k2) saves an addition and loses the digits that a
+            // mean far above the deviation shares with x.
+            const float k2 = -t.y * inv * rs * rs, k1 = -t.x * inv * rs;
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 if (!in(c)) continue;
@@ -352,12 +354,12 @@ __global__ void __launch_bounds__(block_threads<L>(), bwd_threads<VEC, L, NC>() 
                 weights_again(c, wr);
                 const float* w = wr;
                 if constexpr (VEC == 1) {
-                    x[0] = fmaf(y[0] * w[0], rs, fmaf(x[0], k2, k1));
+                    x[0] = fmaf(y[0] * w[0], rs, fmaf(x[0] - mu, k2, k1));
                 } else {
 #pragma unroll
                     for (int v = 0; v < VEC; v += 2) {
                         const F2 gw = mul2(pair<VEC>(y, v), pair<VEC>(w, v));
-                        const F2 o = fma2(gw, both(rs), fma2(pair<VEC>(x, v), both(k2), both(k1)));
+                        const F2 o = fma2(gw, both(rs), fma2(add2(pair<VEC>(x, v), both(-mu)), both(k2), both(k1)));
                         x[v] = o.x;
                         x[v + 1] = o.y;
                     }
