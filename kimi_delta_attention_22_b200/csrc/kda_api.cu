@@ -36,7 +36,11 @@ bool f32path_supports(int D, int V, int C) {
            (C == 16 || C == 32 || C == 64);
 }
 
-kda_status_t from_cuda(cudaError_t e) { return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA; }
+kda_status_t from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return KDA_OK;
+    (void)cudaGetLastError();   // an allocation's or attribute's error stays behind otherwise, for the next launch to report
+    return KDA_ERR_CUDA;
+}
 
 // Query/key heads of a shape (0 means one per value head); -1 if they do not divide H.
 int qk_heads_of(const kda_shape_t* sh) {
@@ -121,9 +125,9 @@ kda_status_t kda_chunk_fwd(const kda_shape_t* sh, const void* q, const void* k, 
     if (!tc) return from_cuda(kda::launch_chunk_f32path(a, bf16, st));
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool pooled = ws == nullptr;   // scratch from the stream-ordered pool (256-byte aligned)
-    if (pooled && cudaMallocAsync(reinterpret_cast<void**>(&ws), lay.bytes, st) != cudaSuccess)
-        return KDA_ERR_CUDA;
-    cudaError_t e = kda::launch_chunk_wy(a, ws, lay, st);
+    cudaError_t e = pooled ? cudaMallocAsync(reinterpret_cast<void**>(&ws), lay.bytes, st) : cudaSuccess;
+    if (e != cudaSuccess) return from_cuda(e);
+    e = kda::launch_chunk_wy(a, ws, lay, st);
     if (e == cudaSuccess) e = kda::launch_chunk_scan(a, ws, lay, st);
     if (pooled) {
         const cudaError_t f = cudaFreeAsync(ws, st);
@@ -143,12 +147,15 @@ kda_status_t kda_chunk_fwd_noalloc(const kda_shape_t* sh, const void* q, const v
         return kda_chunk_fwd(sh, q, k, v, g, beta, S0, cu_seqlens, out, S_T, nullptr, 0, stream);
     if (need > kStaticScratchBytes) return KDA_ERR_TOO_LARGE;
     int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return KDA_ERR_CUDA;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return from_cuda(e);
+    if (dev < 0 || dev >= kMaxDevices) return KDA_ERR_CUDA;
     void* ws = g_static_scratch_addr[dev].load(std::memory_order_acquire);
     if (ws == nullptr) {
         // set-up on this device's first call: the array's device address (loading the
         // module and with it the array, if nothing on this device has yet)
-        if (cudaGetSymbolAddress(&ws, g_static_scratch) != cudaSuccess || ws == nullptr) return KDA_ERR_CUDA;
+        if ((e = cudaGetSymbolAddress(&ws, g_static_scratch)) != cudaSuccess) return from_cuda(e);
+        if (ws == nullptr) return KDA_ERR_CUDA;
         g_static_scratch_addr[dev].store(ws, std::memory_order_release);
     }
     return kda_chunk_fwd(sh, q, k, v, g, beta, S0, cu_seqlens, out, S_T, ws, kStaticScratchBytes, stream);
@@ -237,7 +244,7 @@ kda_status_t kda_recurrent_bwd(const kda_shape_t* sh, const void* q, const void*
     if (e == cudaSuccess) e = cudaMemsetAsync(dbeta, 0, ntok * H * sizeof(float), st);
     if (e == cudaSuccess && gated)
         e = cudaMemsetAsync(dg, 0, ntok * H * (sh->gate == KDA_GATE_CHANNEL ? D : 1) * sizeof(float), st);
-    if (e != cudaSuccess) return KDA_ERR_CUDA;
+    if (e != cudaSuccess) return from_cuda(e);
 
     kda::RecurrentBwdArgs a;
     a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.S0 = S0; a.d_out = d_out; a.d_ST = d_ST;
@@ -306,11 +313,12 @@ kda_status_t kda_chunk_bwd(const kda_shape_t* sh, const void* q, const void* k, 
     if (Hk != H && tok > 0) {   // query/key heads shared by several value heads: summed with atomics
         e = cudaMemsetAsync(dq, 0, (size_t)tok * Hk * sh->d_k * sizeof(float), st);
         if (e == cudaSuccess) e = cudaMemsetAsync(dk, 0, (size_t)tok * Hk * sh->d_k * sizeof(float), st);
-        if (e != cudaSuccess) return KDA_ERR_CUDA;
+        if (e != cudaSuccess) return from_cuda(e);
     }
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool pooled = ws == nullptr;
-    if (pooled && cudaMallocAsync(reinterpret_cast<void**>(&ws), bl.bytes, st) != cudaSuccess) return KDA_ERR_CUDA;
+    if (pooled) e = cudaMallocAsync(reinterpret_cast<void**>(&ws), bl.bytes, st);
+    if (e != cudaSuccess) return from_cuda(e);
     const kda::ChunkArgs fa = kda::forward_args(a);
     e = kda::launch_chunk_wy(fa, ws, bl.fwd, st);
     if (e == cudaSuccess) e = kda::launch_chunk_scans_bwd(a, ws, bl, st);

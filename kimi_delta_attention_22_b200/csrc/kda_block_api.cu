@@ -12,6 +12,7 @@ constexpr long long kMaxRows = 1LL << 31;   // row indexes are 64-bit; grids and
 
 kda_status_t status_of(cudaError_t e) {
     if (e == cudaSuccess) return KDA_OK;
+    (void)cudaGetLastError();   // an allocation's or attribute's error stays behind otherwise, for the next launch to report
     return e == cudaErrorInvalidConfiguration ? KDA_ERR_UNSUPPORTED : KDA_ERR_CUDA;
 }
 
@@ -50,8 +51,9 @@ template <typename F>
 kda_status_t with_workspace(void* workspace, size_t need, cudaStream_t st, F&& go) {
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     const bool pooled = ws == nullptr && need > 0;
-    if (pooled && cudaMallocAsync(reinterpret_cast<void**>(&ws), need, st) != cudaSuccess) return KDA_ERR_CUDA;
-    cudaError_t e = go(ws);
+    cudaError_t e = pooled ? cudaMallocAsync(reinterpret_cast<void**>(&ws), need, st) : cudaSuccess;
+    if (e != cudaSuccess) return status_of(e);
+    e = go(ws);
     if (pooled) {
         const cudaError_t f = cudaFreeAsync(ws, st);
         if (e == cudaSuccess) e = f;
