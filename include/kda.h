@@ -432,7 +432,7 @@ typedef struct {
     int32_t B;           /* sequences (dense); 1 for varlen; step: sequences */
     int32_t T;           /* rows per sequence (dense) or in total (varlen); step: 1 */
     int32_t D;           /* channels */
-    int32_t N;           /* states per channel, 1 to 128 */
+    int32_t N;           /* states per channel, 1 to 128; D * N below 2^29 */
     int32_t G;           /* groups, dividing D */
     int32_t num_seqs;    /* B for dense, len(cu_seqlens) - 1 for varlen */
     int32_t dtype;       /* kda_dtype_t of x, delta, z, Bm, Cm, out and their gradients */

@@ -95,7 +95,8 @@ kda_status_t ssm_check(const kda_ssm_shape_t* sh, bool varlen) {
     for (int64_t v : vec)
         if (v != 0 && v < gn) return KDA_ERR_INVALID_ARG;
     if (!aligned(sh->dev_status, 4)) return KDA_ERR_MISALIGNED;
-    if (sh->N > 128 || (long long)sh->B * sh->T > kMaxRows || (long long)sh->D * sh->N > (1LL << 29) || gn > 0x7fffffffLL)
+    // (the gradient steps over D rows of at least four states with 32-bit strides: D N at 2^29 would overflow them)
+    if (sh->N > 128 || (long long)sh->B * sh->T > kMaxRows || (long long)sh->D * sh->N >= (1LL << 29) || gn > 0x7fffffffLL)
         return KDA_ERR_UNSUPPORTED;
     return KDA_OK;
 }

@@ -473,7 +473,7 @@ cudaError_t step_w(const ConvArgs& a, cudaStream_t s) {
 template <typename T, typename TG, int VEC, int W, bool SILU>
 cudaError_t bwd_one(const ConvArgs& a, cudaStream_t s) {
     const BwdPlan p = bwd_plan(a.M, a.D, VEC);
-    const dim3 grid((unsigned)((a.D + 32 * VEC - 1) / (32 * VEC)), (unsigned)p.K);
+    const dim3 grid((unsigned)((a.D + 32LL * VEC - 1) / (32 * VEC)), (unsigned)p.K);
     constexpr int sums = (int)sizeof(float) * kBwdWarps * (W + 1) * VEC * 32;
     constexpr int ring = VEC > 1 ? kBwdAhead * kU * 32 * kBwdWarps * VEC * (int)(sizeof(T) + sizeof(TG)) : 0;
     constexpr int smem = sums > ring ? sums : ring;
