@@ -206,11 +206,13 @@ def _out(given, what, shape, dtype, device, like=None):
     return given, _want(given, what, shape, dtype, device)
 
 
-def _grads(given, names):
-    """The caller's gradient buffers by name."""
+def _grads(given, **computed):
+    """The caller's gradient buffers by name; `computed` tells of every gradient whether the call writes it."""
     given = given or {}
-    if unknown := set(given) - set(names):
-        raise ValueError(f"unknown gradients {sorted(unknown)}: expected some of {names}")
+    if unknown := set(given) - set(computed):
+        raise ValueError(f"unknown gradients {sorted(unknown)}: expected some of {tuple(computed)}")
+    if idle := sorted(k for k, v in given.items() if v is not None and not computed[k]):
+        raise ValueError(f"buffers for gradients that this call does not compute: {idle} (their input is None, or they are not wanted)")
     return given
 
 
@@ -295,7 +297,7 @@ def kda_conv_bwd(x, weight, d_out, bias=None, state=None, d_final_state=None, cu
     dev = _cuda(x, "x")
     D, W, w, b, xs = _conv_common(x, weight, bias, dev, False)
     B, T, N = _batch(x, cu_seqlens, dev)
-    grads = _grads(grads, ("dx", "dweight", "dbias", "dstate"))
+    grads = _grads(grads, dx=True, dweight=True, dbias=bias is not None, dstate=want_dstate)
     st = (N, max(W - 1, 0), D)
     sp = _want(state, "state", st, x.dtype, dev)
     dsp = _want(d_final_state, "d_final_state", st, x.dtype, dev)
@@ -406,7 +408,8 @@ def kda_ssm_bwd(x, dt, A, B, C, d_out, D=None, z=None, dt_bias=None, h0=None, d_
     dev = _cuda(x, "x")
     Dc, N, G, st, p = _ssm_common(x, dt, A, B, C, D, z, dt_bias, dev, False)
     b, T, n = _batch(x, cu_seqlens, dev)
-    grads = _grads(grads, ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "ddt_bias", "dh0"))
+    grads = _grads(grads, dx=True, ddt=True, dA=True, dB=True, dC=True, dD=D is not None, dz=z is not None,
+                   ddt_bias=dt_bias is not None, dh0=want_dh0)
     hp = _want(h0, "h0", (n, Dc, N), torch.float32, dev)
     dtp = _want(d_hT, "d_hT", (n, Dc, N), torch.float32, dev)
     dop = _want(d_out, "d_out", x.shape, x.dtype, dev)
@@ -491,7 +494,7 @@ def kda_layer_norm_bwd(d_out, x, mean, rstd, weight=None, want_params: bool = Tr
         G, inner, pshape = groups, 2, (groups, D)
         rows = x.numel() // (G * D) if G * D else 0
     xs = _strided(x, "x", x.shape, x.dtype, dev, inner, G * D)
-    grads = _grads(grads, ("dx", "dweight", "dbias"))
+    grads = _grads(grads, dx=True, dweight=want_params, dbias=want_params)
     dp = _want(d_out, "d_out", x.shape, x.dtype, dev)
     mp = _want(mean, "mean", x.shape[:-1], torch.float32, dev)
     rp = _want(rstd, "rstd", x.shape[:-1], torch.float32, dev)
