@@ -245,6 +245,14 @@ struct Place {
         if (n(m) + 1 < a.N) v.y = at[1];
         return v;
     }
+    // A log2(e); -1 for the states that pad N: an infinite step then gives their decay as 0, where
+    // e^{inf 0} would be NaN and reach the sums over the states.
+    __device__ __forceinline__ F2 rates(const SsmArgs& a, int k, int m) const {
+        F2 v = mul2(get(a.A, 0, a, k, m), both(kLog2e));
+        if (n(m) >= a.N) v.x = -1.0f;
+        if (n(m) + 1 >= a.N) v.y = -1.0f;
+        return v;
+    }
     __device__ __forceinline__ void put(float* p, long long q, const SsmArgs& a, int k, int m, F2 v) const {
         if (p == nullptr || !live[k]) return;
         float* at = p + (q * a.D + d[k]) * a.N + n(m);
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 4) ssm_bwd_summary_kernel(SsmArgs a,
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            A2[k][m] = mul2(at.get(a.A, 0, a, k, m), both(kLog2e));
+            A2[k][m] = at.rates(a, k, m);
             h[k][m] = g[k][m] = F2{0.f, 0.f};
             p[k][m] = F2{1.f, 1.f};
         }
@@ -412,7 +420,7 @@ __global__ void __launch_bounds__(128) ssm_bwd_join_kernel(SsmArgs a, int NP, lo
     if (i >= DN) return;
     const long long d = i / NP;
     const int n = (int)(i - d * NP);
-    const float A2 = n < a.N ? a.A[d * a.N + n] * kLog2e : 0.f;
+    const float A2 = n < a.N ? a.A[d * a.N + n] * kLog2e : -1.0f;
     const bool fwd = blockIdx.y == 0;
     float* v = fwd ? hseg : rseg;
     float c = 0.f;
@@ -526,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 3) ssm_bwd_grad_kernel(SsmArgs a, Se
     for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            A2[k][m] = mul2(at.get(a.A, 0, a, k, m), both(kLog2e));
+            A2[k][m] = at.rates(a, k, m);
             dh[k][m] = at.load(rseg, sg, a.D, k, m);
             dA[k][m] = F2{0.f, 0.f};
         }
