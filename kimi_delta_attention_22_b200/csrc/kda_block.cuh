@@ -92,7 +92,7 @@ struct NormArgs {
 
 cudaError_t launch_norm_fwd(const NormArgs& a, bool bf16, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t s);
-size_t norm_bwd_workspace_bytes(long long rows, int G, int D);
+size_t norm_bwd_workspace_bytes(long long rows, int G, int D, bool bf16);
 
 // out_i[c] = sum_k part[k][off_i + c], k in order within each of sixteen interleaved
 // partial sums: the second stage of a parameter gradient's reduction over the rows.

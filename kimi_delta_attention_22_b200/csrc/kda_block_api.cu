@@ -317,7 +317,7 @@ kda_status_t kda_layer_norm_fwd(const kda_norm_shape_t* sh, const void* x, const
 
 size_t kda_layer_norm_bwd_workspace_size(const kda_norm_shape_t* sh) {
     if (norm_check(sh) != KDA_OK) return 0;
-    return kda::norm_bwd_workspace_bytes(sh->rows, sh->groups, sh->D);
+    return kda::norm_bwd_workspace_bytes(sh->rows, sh->groups, sh->D, sh->dtype == KDA_BF16);
 }
 
 kda_status_t kda_layer_norm_bwd(const kda_norm_shape_t* sh, const void* d_out, const void* x, const float* weight,

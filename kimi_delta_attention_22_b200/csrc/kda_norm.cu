@@ -449,12 +449,16 @@ cudaError_t fwd_one(const NormArgs& a, cudaStream_t s) {
     k<<<(unsigned)grid, block_threads<L>(), 0, s>>>(a);
     return cudaGetLastError();
 }
+template <int VEC, int L, int NC>
+int layout_ctas(long long rows, int G) {
+    return bwd_ctas(rows, G, cta_rows<L>(), block_threads<L>(), bwd_threads<VEC, L, NC>());
+}
 template <typename T, int VEC, int L, int NC>
 cudaError_t bwd_one(const NormArgs& a, cudaStream_t s) {
     constexpr int bytes = NC * block_threads<L>() * (kStages * 32 + VEC * 4);
     constexpr bool RING = VEC > 1 && bytes <= 200 * 1024;
     constexpr int smem = RING ? bytes : 0;
-    const int K = bwd_ctas(a.rows, a.G, cta_rows<L>(), block_threads<L>(), bwd_threads<VEC, L, NC>());
+    const int K = layout_ctas<VEC, L, NC>(a.rows, a.G);
     const bool full = VEC > 1 && a.D == L * NC * VEC;
     auto k = full ? norm_bwd_kernel<T, VEC, L, NC, RING, (VEC > 1)> : norm_bwd_kernel<T, VEC, L, NC, RING, false>;
     cudaError_t e;
@@ -474,16 +478,17 @@ bool norm_vec(const NormArgs& a, int el) {
 
 // Lanes per row and accesses per lane: few lanes that hold the row in registers, so that
 // short rows share a warp and no row waits for a barrier that it does not need.
-template <typename T, bool BWD>
-cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
-    constexpr int V = 16 / sizeof(T);
-#define KDA_NORM(VEC, L, NC)                                \
-    do {                                                    \
-        if constexpr (BWD) return bwd_one<T, VEC, L, NC>(a, s); \
-        else return fwd_one<T, VEC, L, NC>(a, s);           \
-    } while (0)
-    if (norm_vec(a, sizeof(T))) {
-        const int n = a.D / V;   // accesses per row
+// f(Layout<..>{}) is called for the layout of rows of D elements of EL bytes, with or without vector accesses.
+template <int VEC_, int L_, int NC_>
+struct Layout {
+    static constexpr int VEC = VEC_, L = L_, NC = NC_;
+};
+template <int EL, bool BWD, typename F>
+auto with_layout(bool vec, int D, F&& f) {
+    constexpr int V = 16 / EL;
+#define KDA_NORM(VEC, L, NC) return f(Layout<VEC, L, NC>{})
+    if (vec) {
+        const int n = D / V;   // accesses per row
         if (n <= 8) KDA_NORM(V, 8, 1);
         if (n <= 16) KDA_NORM(V, 8, 2);
         if (n <= 32) KDA_NORM(V, 32, 1);
@@ -519,23 +524,41 @@ cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
             KDA_NORM(V, 1024, 4);
         }
     }
-    if (a.D <= 32) KDA_NORM(1, 8, 4);
-    if (a.D <= 256) KDA_NORM(1, 32, 8);
+    if (D <= 32) KDA_NORM(1, 8, 4);
+    if (D <= 256) KDA_NORM(1, 32, 8);
     // Element accesses: CTAs of few warps with long runs per lane, several of them per SM (one CTA of
     // 1024 threads has nothing to do while its sums meet).  bf16, 8192 x 4095: forward 147 us with
     // 1024 lanes, 40 us with 256; gradient 184 and 97 us, of which half by its scalar arithmetic.
-    if (a.D <= 512) KDA_NORM(1, 64, 8);
+    if (D <= 512) KDA_NORM(1, 64, 8);
     if constexpr (BWD) {
-        if (a.D <= 1024) KDA_NORM(1, 128, 8);
+        if (D <= 1024) KDA_NORM(1, 128, 8);
     } else {
-        if (a.D <= 1024) KDA_NORM(1, 64, 16);
+        if (D <= 1024) KDA_NORM(1, 64, 16);
     }
-    if (a.D <= 2048) KDA_NORM(1, 128, 16);
-    if (a.D <= 4096) KDA_NORM(1, 256, 16);
-    if (a.D <= 8192) KDA_NORM(1, 512, 16);
-    if (a.D <= 16384) KDA_NORM(1, 1024, 16);
+    if (D <= 2048) KDA_NORM(1, 128, 16);
+    if (D <= 4096) KDA_NORM(1, 256, 16);
+    if (D <= 8192) KDA_NORM(1, 512, 16);
+    if (D <= 16384) KDA_NORM(1, 1024, 16);
     KDA_NORM(1, 1024, 32);
 #undef KDA_NORM
+}
+
+template <typename T, bool BWD>
+cudaError_t norm_t(const NormArgs& a, cudaStream_t s) {
+    return with_layout<sizeof(T), BWD>(norm_vec(a, sizeof(T)), a.D, [&](auto l) {
+        using Lay = decltype(l);
+        if constexpr (BWD) return bwd_one<T, Lay::VEC, Lay::L, Lay::NC>(a, s);
+        else return fwd_one<T, Lay::VEC, Lay::L, Lay::NC>(a, s);
+    });
+}
+
+// CTAs (partial sums) of the gradient's two possible layouts: the pointers' alignment decides between them.
+template <int EL>
+int most_ctas(long long rows, int G, int D) {
+    const auto ctas = [&](auto l) { return layout_ctas<decltype(l)::VEC, decltype(l)::L, decltype(l)::NC>(rows, G); };
+    const int one = with_layout<EL, true>(false, D, ctas);
+    const int vec = D % (16 / EL) == 0 ? with_layout<EL, true>(true, D, ctas) : 0;
+    return one > vec ? one : vec;
 }
 
 }  // namespace
@@ -555,9 +578,8 @@ cudaError_t launch_norm_bwd(const NormArgs& a, bool bf16, cudaStream_t s) {
     return bf16 ? norm_t<__nv_bfloat16, true>(a, s) : norm_t<float, true>(a, s);
 }
 
-// The partial sums of the most CTAs that any layout of the row would use.
-size_t norm_bwd_workspace_bytes(long long rows, int G, int D) {
-    return sizeof(float) * 2 * (size_t)G * D * bwd_ctas(rows, G, 1, 64, 1024);
+size_t norm_bwd_workspace_bytes(long long rows, int G, int D, bool bf16) {
+    return sizeof(float) * 2 * (size_t)G * D * (bf16 ? most_ctas<2>(rows, G, D) : most_ctas<4>(rows, G, D));
 }
 
 }  // namespace kda
