@@ -95,8 +95,14 @@ __device__ __forceinline__ void load_params(const float* p, float* o) {
 template <int VEC>
 __device__ __forceinline__ F2 pair(const float* f, int v) { return F2{f[v], f[v + 1]}; }
 
+// Two rows of 32 elements per lane would take 130 registers, which leaves one CTA of 256 threads per SM
+// instead of two (bf16, 32768 x 1024: 39 us instead of 27).  The other layouts are not bounded (0): the
+// compiler spends more registers under a bound of one or two CTAs (32768 x 4096: 132 us instead of 103).
+template <int VEC, int L, int NC>
+constexpr int fwd_ctas() { return L <= 32 && VEC * NC == 32 ? 2 : 0; }
+
 template <typename T, int VEC, int L, int NC, bool FULL>
-__global__ void __launch_bounds__(block_threads<L>()) norm_fwd_kernel(NormArgs a) {
+__global__ void __launch_bounds__(block_threads<L>(), fwd_ctas<VEC, L, NC>()) norm_fwd_kernel(NormArgs a) {
     constexpr int NI = rows_per_item<L, NC>();
     __shared__ float2 buf[L > 32 ? 2 * (L / 32) : 1];
     int turn = 0;
