@@ -474,9 +474,11 @@ kda_status_t kda_ssm_step(const kda_ssm_shape_t* shape, const void* x, const voi
  * [rows, D], dB, dC [rows, G, N], dz [rows, D] (with z; else NULL) of dtype, and fp32 dA
  * [D, N], dDskip [D] (with Dskip; else NULL), ddelta_bias [D] (with delta_bias; else
  * NULL), dh0 [num_seqs, D, N] or NULL (not wanted).  The states are computed again from
- * the inputs; nothing is kept from the forward call.  The workspace holds a state for every
- * four rows and, per block of 64 channels (at N = 16), the rows' partial sums of dB and dC:
- * about 20 bytes per row and channel at N = 16, in proportion to N.
+ * the inputs; nothing is kept from the forward call.  With P the states rounded up to 4, 8, 16,
+ * 32, 64 or 128, the workspace holds a state of P for every four rows, the rows' partial sums of
+ * dB and dC for every 1024 / P channels of a group, and states and parameter sums for segments
+ * of 32 to 256 rows: per row and channel P + 1 + N P / 128 bytes and a few more for the segments
+ * (8192 rows, 2048 channels: 21 bytes at N = 16, 43 at 32, 100 at 64, 263 at 128).
  */
 kda_status_t kda_ssm_bwd(const kda_ssm_shape_t* shape, const void* x, const void* delta,
                          const float* A, const void* Bm, const void* Cm, const float* Dskip,

@@ -10,9 +10,9 @@
 // run of rows with the window of earlier inputs in registers, so that each input is read once,
 // plus W - 1 rows in front of each run.  The rows ahead are copied asynchronously into slots of
 // shared memory that only this thread reads: enough bytes are under way without holding
-// registers.  bf16: forward of 65536 x 4096, 4 taps, 210 us, 5.1 TB/s; gradient of
-// 8192 x 6144 74 us, 4.1 TB/s (16 warps per SM, which its 126 registers leave, issue in half of
-// their slots); a step of 256 x 4096 6 us.
+// registers.  bf16: forward of 65536 x 4096, 4 taps, 209 us, 5.1 TB/s (its bound of three CTAs per SM
+// spills 36 bytes, fp32 88); gradient of 8192 x 6144 74 us, 4.1 TB/s (16 warps per SM, which its 126
+// registers leave, issue in half of their slots); a step of 256 x 4096 4 us in a captured graph.
 //
 // The tap count W is a template parameter: the window holds the W - 1 rows in front of the
 // newest and no others (an unused tap of zero would make NaN of an infinity outside the window).
@@ -420,13 +420,14 @@ struct BwdPlan {
     int K;
     long long run, nruns;
 };
-// One run of consecutive rows per warp, as many CTAs as are resident at once (two per SM): the
-// rows divide evenly and the W - 1 rows behind a run, computed twice, are few.
+// One run of consecutive rows per warp, as many CTAs as are resident at once (two per SM) but no more
+// than one per 128 rows: the rows divide evenly and the W - 1 rows behind a run, computed twice, are
+// few.  (Below 128 rows in all the one CTA's runs are shorter, down to a row.)
 BwdPlan bwd_plan(long long M, int D, int vec) {
     BwdPlan p;
     const long long nblk = (D + 32LL * vec - 1) / (32LL * vec);
     long long K = 2 * kSMs / nblk;
-    const long long most = (M + 16LL * kBwdWarps - 1) / (16LL * kBwdWarps);   // at least 16 rows per run
+    const long long most = (M + 16LL * kBwdWarps - 1) / (16LL * kBwdWarps);
     if (K > most) K = most;
     p.K = (int)(K < 1 ? 1 : K);
     p.run = (M + (long long)p.K * kBwdWarps - 1) / ((long long)p.K * kBwdWarps);

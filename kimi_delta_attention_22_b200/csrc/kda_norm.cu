@@ -11,9 +11,9 @@
 // registers: the variance is the exact sum over (x - mean)^2, not a difference of moments.
 // out may be x, and dx x or d_out: these are read by plain loads (or copies ahead, of other rows).
 // The gradient's CTAs walk rows of one group with the parameter gradients of the lane's
-// columns in registers, and write one partial sum each.  bf16: gradient of 65536 x 4096
-// 305 to 325 us, 4.9 to 5.3 TB/s; per-head forward of 131072 x 128 16 us, 4.3 TB/s (of which
-// launch and tail are 4 us).
+// columns in registers, and write one partial sum each.  bf16, in a captured graph: gradient of
+// 65536 x 4096 285 us, 5.7 TB/s (305 to 325 us as single calls, by card); per-head forward of
+// 131072 x 128 14 to 15 us, 4.6 TB/s (a call takes 16.5 us, which is the host's time).
 #include "kda_block.cuh"
 
 namespace kda {
@@ -76,8 +76,8 @@ __device__ __forceinline__ long long div_by(long long a, int b) {   // a >= 0; 3
 // Whether access c of a lane lies in the row.  The layouts (norm_t) give a row of vector accesses,
 // and every row of more than 32 lanes, more than half of the lanes' accesses, so only the upper
 // half of them is ever compared; FULL: the row fills all of them.  The comparisons cost more
-// than they look: each keeps the access apart as a branch of its own (65536 x 4096 gradient:
-// 339 us with all, 294 us with none).
+// than they look: each keeps the access apart as a branch of its own (65536 x 4096 gradient in a
+// captured graph: 329 us with all, 285 us with none).
 template <int VEC, int L, int NC, bool FULL>
 __device__ __forceinline__ bool in_row(int c, int lane, int D) {
     if constexpr (FULL) return true;
@@ -200,7 +200,7 @@ constexpr int kStages = 3;   // rows in the ring, one of them being worked on
 
 // grid (K, G): CTA (k, g) walks rows k, k + K, .. (times the rows it holds at once) of group g.
 // RING: x and d_out of the next rows are copied ahead (STG - 1 rows) into slots of shared memory
-// that only the copying thread reads; without it the next row waits in registers.  A row is
+// that only the copying thread reads; without it a row is loaded in the turn that uses it.  A row is
 // gone over twice in registers as it was loaded, once for its sums and the parameters'
 // gradients, once for dx: unpacking again costs less than the registers of fp32 copies.
 // Threads per SM that the registers are held to where two accesses of a lane leave the choice:
