@@ -360,7 +360,8 @@ kda_status_t kda_selftest_bounded_wait(int32_t* dev_status, uint32_t budget_us, 
  *     may read what others have overwritten.  In place are taken: out of a step on x, delta or z
  *     and out or dx of layer norm on x, each with rows at the same distance, dx of layer norm
  *     on d_out, dh0 on h0, and a parameter's gradient on the parameter.
- *     Overlaps that do not start at the same address are the caller's to avoid.
+ *     Two outputs at one address are refused as well.  Overlaps that do not start at the same
+ *     address are the caller's to avoid.
  *   - Every pointer needs its element's alignment.  Where the pointers, strides and
  *     row lengths are multiples of 16 bytes, 16-byte accesses are used.
  *   - Activations and their gradients have the element type `dtype` (fp32 or bf16);

@@ -34,7 +34,14 @@ bool in_place(std::initializer_list<const void*> outs, std::initializer_list<con
             if (o != nullptr && o == i) return true;
     return false;
 }
-// The same for an output whose elements are stored by the thread that read the input's elements at
+// Whether two outputs start at the same address.
+bool one_place(std::initializer_list<const void*> outs) {
+    for (const void* const* o = outs.begin(); o != outs.end(); ++o)
+        for (const void* const* p = outs.begin(); p != o; ++p)
+            if (*o != nullptr && *o == *p) return true;
+    return false;
+}
+// As in_place for an output whose elements are stored by the thread that read the input's elements at
 // the same index: in place is then right where consecutive rows of both lie `row` elements apart.
 bool rows_shifted(const void* out, const void* in, long long rows, long long stride, long long row) {
     return out != nullptr && out == in && rows > 1 && stride != row;
@@ -148,7 +155,8 @@ kda_status_t kda_conv_fwd(const kda_conv_shape_t* sh, const void* x, const float
     if (!aligned(x, el) || !aligned(weight, 4) || !aligned(bias, 4) || !aligned(state0, el) || !aligned(cu_seqlens, 4) ||
         !aligned(out, el) || !aligned(stateT, el))
         return KDA_ERR_MISALIGNED;
-    if (in_place({stateT}, {state0}) || (a.M > 0 && in_place({out, stateT}, {x, state0, weight, bias}))) return KDA_ERR_INVALID_ARG;
+    if (in_place({stateT}, {state0}) || (a.M > 0 && (in_place({out, stateT}, {x, state0, weight, bias}) || one_place({out, stateT}))))
+        return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return status_of(kda::launch_conv_fwd(a, sh->dtype == KDA_BF16, sh->activation == 1, static_cast<cudaStream_t>(stream)));
 }
@@ -198,7 +206,7 @@ kda_status_t kda_conv_bwd(const kda_conv_shape_t* sh, const void* x, const float
     // runs read rows, states and their gradients that others store gradients over (those of the
     // parameters are stored behind the last read of anything)
     if (in_place({dstate0}, {state0, d_stateT}) ||
-        (a.M > 0 && in_place({dx, dstate0}, {x, d_out, state0, d_stateT, weight, bias})))
+        (a.M > 0 && (in_place({dx, dstate0}, {x, d_out, state0, d_stateT, weight, bias}) || one_place({dx, dweight, dbias, dstate0}))))
         return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.part = reinterpret_cast<float*>(ws);
@@ -226,7 +234,8 @@ kda_status_t kda_ssm_fwd(const kda_ssm_shape_t* sh, const void* x, const void* d
     const size_t need = kda_ssm_fwd_workspace_size(sh, cu_seqlens != nullptr);
     c = check_workspace(workspace, workspace_bytes, need);
     if (c != KDA_OK) return c;
-    if (in_place({hT}, {h0}) || (a.M > 0 && in_place({out, hT}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, h0}))) return KDA_ERR_INVALID_ARG;
+    if (in_place({hT}, {h0}) || (a.M > 0 && (in_place({out, hT}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, h0}) || one_place({out, hT}))))
+        return KDA_ERR_INVALID_ARG;
     if (sh->num_seqs == 0) return KDA_OK;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.ws = ws;
@@ -286,7 +295,8 @@ kda_status_t kda_ssm_bwd(const kda_ssm_shape_t* sh, const void* x, const void* d
     // (and the parameters' gradients are stored behind the last read of anything)
     if (in_place({dh0}, {d_hT}) ||
         (a.M > 0 && (in_place({dx, ddelta, dz, dB, dC}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, h0, d_out, d_hT}) ||
-                     in_place({dh0}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, d_out}))))
+                     in_place({dh0}, {x, delta, z, Bm, Cm, A, Dskip, delta_bias, d_out}) ||
+                     one_place({dx, ddelta, dA, dB, dC, dDskip, dz, ddelta_bias, dh0}))))
         return KDA_ERR_INVALID_ARG;
     return with_workspace(workspace, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.ws = ws;
@@ -305,7 +315,8 @@ kda_status_t kda_layer_norm_fwd(const kda_norm_shape_t* sh, const void* x, const
         !aligned(rstd, 4))
         return KDA_ERR_MISALIGNED;
     if (sh->rows == 0) return KDA_OK;
-    if (in_place({out, mean, rstd}, {weight, bias}) || in_place({mean, rstd}, {x})) return KDA_ERR_INVALID_ARG;
+    if (in_place({out, mean, rstd}, {weight, bias}) || in_place({mean, rstd}, {x}) || one_place({out, mean, rstd}))
+        return KDA_ERR_INVALID_ARG;
     kda::NormArgs a{};
     a.x = x; a.w = weight; a.b = bias; a.out = out; a.mean = mean; a.rstd = rstd;
     a.rows = sh->rows; a.G = sh->groups; a.D = sh->D; a.eps = sh->eps;
@@ -341,7 +352,8 @@ kda_status_t kda_layer_norm_bwd(const kda_norm_shape_t* sh, const void* d_out, c
     a.rows = sh->rows; a.G = sh->groups; a.D = sh->D;
     const long long row = (long long)sh->groups * sh->D;
     a.xs = sh->x_stride != 0 ? sh->x_stride : row;
-    if (a.rows > 0 && (in_place({dx}, {weight, mean, rstd}) || rows_shifted(dx, x, a.rows, a.xs, row))) return KDA_ERR_INVALID_ARG;
+    if (a.rows > 0 && (in_place({dx}, {weight, mean, rstd}) || one_place({dx, dweight, dbias}) || rows_shifted(dx, x, a.rows, a.xs, row)))
+        return KDA_ERR_INVALID_ARG;
     return with_workspace(need ? workspace : nullptr, need, static_cast<cudaStream_t>(stream), [&](uint8_t* ws) {
         a.part = reinterpret_cast<float*>(ws);
         return kda::launch_norm_bwd(a, sh->dtype == KDA_BF16, static_cast<cudaStream_t>(stream));

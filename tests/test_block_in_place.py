@@ -126,6 +126,38 @@ def test_norm_gradient(lib, out, inp, stride):
     assert lib.kda_layer_norm_bwd(ctypes.byref(sh), *a.values(), need, None) == 1
 
 
+def pairs(names):
+    return [(a, b) for i, a in enumerate(names) for b in names[i + 1:]]
+
+
+def test_two_outputs_at_one_address(lib):
+    sh = kda.ConvShape(2, 3, 16, 2, 4, kda.KDA_F32, 0, 1, 0, None)
+    a = other(1, ("x", "w", "b", "state0", "out", "fin"), dict(fin="out"))
+    assert lib.kda_conv_fwd(ctypes.byref(sh), a["x"], a["w"], a["b"], a["state0"], None, a["out"], a["fin"], None) == 1
+    need = lib.kda_conv_bwd_workspace_size(ctypes.byref(sh))
+    for p, q in pairs(("dx", "dw", "db", "dst")):
+        a = other(1, ("x", "w", "b", "dy", "dx", "dw", "db", "dst", "ws"), {q: p})
+        assert lib.kda_conv_bwd(ctypes.byref(sh), a["x"], a["w"], a["b"], None, None, a["dy"], None, a["dx"], a["dw"], a["db"],
+                                a["dst"], a["ws"], need, None) == 1, (p, q)
+    sh = kda.SsmShape(2, 8, 16, 16, 1, 2, kda.KDA_F32, 1, 0, 0, 0, 0, 0, None)
+    a = other(1, SSM_IN + ("out", "hT"), dict(hT="out"))
+    assert lib.kda_ssm_fwd(ctypes.byref(sh), *(a[n] for n in SSM_IN), None, None, a["out"], a["hT"], None, 0, None) == 1
+    need = lib.kda_ssm_bwd_workspace_size(ctypes.byref(sh), 0)
+    outs = ("dx", "ddt", "dA", "dB", "dC", "dD", "dz", "db", "dh0")
+    for p, q in pairs(outs):
+        a = other(1, SSM_IN + ("dy",) + outs + ("ws",), {q: p})
+        assert lib.kda_ssm_bwd(ctypes.byref(sh), *(a[n] for n in SSM_IN), None, None, a["dy"], None, *(a[n] for n in outs), a["ws"],
+                               need, None) == 1, (p, q)
+    sh = kda.NormShape(3, 1, 64, kda.KDA_F32, 1e-5, 0)
+    for p, q in pairs(("out", "mean", "rstd")):
+        a = other(1, ("x", "w", "b", "out", "mean", "rstd"), {q: p})
+        assert lib.kda_layer_norm_fwd(ctypes.byref(sh), *a.values(), None) == 1, (p, q)
+    need = lib.kda_layer_norm_bwd_workspace_size(ctypes.byref(sh))
+    for p, q in pairs(("dx", "dw", "db")):
+        a = other(1, ("dy", "x", "w", "mean", "rstd", "dx", "dw", "db", "ws"), {q: p})
+        assert lib.kda_layer_norm_bwd(ctypes.byref(sh), *a.values(), need, None) == 1, (p, q)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype,D", [(BF, 64), (F32, 64), (BF, 13), (F32, 300), (BF, 4096)])
 def test_what_may_be_in_place(dtype, D):
